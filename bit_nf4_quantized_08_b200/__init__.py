@@ -8,14 +8,22 @@ quantization of the block constants, as a C-ABI CUDA library
 from ._lib import QloraError, QLORA_OK, QLORA_ERR_INVALID_ARG, QLORA_ERR_UNSUPPORTED, \
     QLORA_ERR_CUDA, QLORA_ERR_TIMEOUT, QLORA_ERR_WORKSPACE, QLORA_ERR_BOUNDS, QLORA_STATIC_QUANTIZE_MAX_ELEMS  # noqa: F401
 from .api import (  # noqa: F401
+    Dropout,
     NF4Weight,
     PagedBuffer,
     qlora_adamw_step,
     qlora_debug_inject,
     qlora_dq_encode,
+    qlora_dropout,
     qlora_fused_linear_bwd,
+    qlora_fused_linear_dropout_bwd,
+    qlora_fused_linear_dropout_fwd,
+    qlora_fused_linear_dropout_workspace,
     qlora_fused_linear_fwd,
     qlora_fused_linear_workspace,
+    qlora_gated_linear_bwd,
+    qlora_gated_linear_fwd,
+    qlora_gated_linear_workspace,
     qlora_get_last_error,
     qlora_linear_bwd,
     qlora_linear_fwd,

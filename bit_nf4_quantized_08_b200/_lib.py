@@ -28,6 +28,7 @@ QLORA_F32 = 0
 QLORA_BF16 = 1
 CODE_TYPES = {"nf4": 0, "fp4": 1}
 DQ_TYPES = {"int8": 0, "e4m3": 1}
+ACT_TYPES = {"silu": 0, "gelu_tanh": 1}
 QLORA_STATIC_QUANTIZE_MAX_ELEMS = 1 << 26
 
 # Every function the header declares (checked against the header by the tests).
@@ -42,6 +43,13 @@ EXPORTS = (
     "qlora_fused_linear_workspace",
     "qlora_fused_linear_fwd",
     "qlora_fused_linear_bwd",
+    "qlora_dropout",
+    "qlora_fused_linear_dropout_workspace",
+    "qlora_fused_linear_dropout_fwd",
+    "qlora_fused_linear_dropout_bwd",
+    "qlora_gated_linear_workspace",
+    "qlora_gated_linear_fwd",
+    "qlora_gated_linear_bwd",
     "qlora_lora_merge",
     "qlora_lora_unmerge",
     "qlora_adamw_step",
@@ -100,6 +108,17 @@ class CAdamWConfig(ctypes.Structure):
     ]
 
 
+class CDropoutConfig(ctypes.Structure):
+    """Mirror of ``qlora_dropout_config``."""
+
+    _fields_ = [
+        ("p", ctypes.c_float),
+        ("seed", ctypes.c_uint64),
+        ("offset", ctypes.c_uint64),
+        ("offset_dev", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -136,6 +155,22 @@ def lib() -> ctypes.CDLL:
     L.qlora_fused_linear_fwd.restype = i32
     L.qlora_fused_linear_bwd.argtypes = [vp, vp, i64, W, i32, vp, vp, i32, f32, vp, vp, vp, vp, sz, vp]
     L.qlora_fused_linear_bwd.restype = i32
+    D = ctypes.POINTER(CDropoutConfig)
+    L.qlora_dropout.argtypes = [vp, i32, i64, D, vp, vp]
+    L.qlora_dropout.restype = i32
+    L.qlora_fused_linear_dropout_workspace.argtypes = [i64, W, i32, i32, i32]
+    L.qlora_fused_linear_dropout_workspace.restype = sz
+    L.qlora_fused_linear_dropout_fwd.argtypes = [vp, i64, W, i32, vp, vp, i32, f32, D, vp, vp, sz, vp]
+    L.qlora_fused_linear_dropout_fwd.restype = i32
+    L.qlora_fused_linear_dropout_bwd.argtypes = [vp, vp, i64, W, i32, vp, vp, i32, f32, D, vp, i32, vp, vp, vp, sz,
+                                                 vp]
+    L.qlora_fused_linear_dropout_bwd.restype = i32
+    L.qlora_gated_linear_workspace.argtypes = [i64, W, i32, i32]
+    L.qlora_gated_linear_workspace.restype = sz
+    L.qlora_gated_linear_fwd.argtypes = [vp, i64, W, vp, vp, i32, f32, i32, D, vp, vp, vp, sz, vp]
+    L.qlora_gated_linear_fwd.restype = i32
+    L.qlora_gated_linear_bwd.argtypes = [vp, vp, vp, i64, W, vp, vp, i32, f32, i32, D, vp, i32, vp, vp, vp, sz, vp]
+    L.qlora_gated_linear_bwd.restype = i32
     L.qlora_lora_merge.argtypes = [W, vp, vp, i32, f32, vp, vp]
     L.qlora_lora_merge.restype = i32
     L.qlora_lora_unmerge.argtypes = [vp, i64, i64, vp, vp, i32, f32, vp, vp]

@@ -14,7 +14,8 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from ._lib import CAdamWConfig, CNF4Weight, CODE_TYPES, DQ_TYPES, QLORA_BF16, QLORA_F32, check, lib
+from ._lib import ACT_TYPES, CAdamWConfig, CDropoutConfig, CNF4Weight, CODE_TYPES, DQ_TYPES, QLORA_BF16, QLORA_F32, \
+    check, lib
 
 BLOCKSIZE = 64
 DQ_BLOCK = 256
@@ -234,6 +235,212 @@ def qlora_fused_linear_bwd(dY: torch.Tensor, X: torch.Tensor, w: NF4Weight, nseg
     check(lib().qlora_fused_linear_bwd(_ptr(dY), _ptr(X), M, ctypes.byref(cw), nseg, _ptr(A), _ptr(B), r,
                                        float(scale), _ptr(dX) if want_dx else None, _ptr(dA), _ptr(dB),
                                        _ptr(wsb), wsb.numel(), _stream()), "qlora_fused_linear_bwd")
+    return dX, dA, dB
+
+
+@dataclass
+class Dropout:
+    """A dropout configuration: drop probability p, the generator's seed and
+    the call's offset (one offset, one mask).  ``offset_dev``, a one-element
+    int64 CUDA tensor, is added to the offset when the kernels run, so that a
+    captured graph draws a new mask at each replay after the program has
+    advanced it."""
+
+    p: float
+    seed: int
+    offset: int = 0
+    offset_dev: torch.Tensor | None = None
+
+    def c_struct(self) -> CDropoutConfig:
+        for name, v in (("seed", self.seed), ("offset", self.offset)):
+            if not 0 <= int(v) < 1 << 64:
+                raise ValueError(f"dropout {name} must be an unsigned 64-bit number")
+        t = self.offset_dev
+        if t is not None and (t.dtype != torch.int64 or t.numel() != 1 or not t.is_cuda):
+            raise ValueError("offset_dev must be a one-element int64 CUDA tensor")
+        return CDropoutConfig(float(self.p), int(self.seed), int(self.offset), _ptr(t))
+
+
+def _drop_arg(d: Dropout | None, device):
+    """ctypes argument of an optional dropout."""
+    if d is None:
+        return None
+    if d.offset_dev is not None and d.offset_dev.device != device:
+        raise ValueError("offset_dev must be on the tensors' device")
+    return ctypes.byref(d.c_struct())
+
+
+def _expect(t: torch.Tensor | None, name: str, shape, dtype, device, optional: bool = False) -> None:
+    """A dense CUDA tensor of this shape and type on this device."""
+    if t is None:
+        if optional:
+            return
+        raise ValueError(f"{name} is missing")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+_GRAD_DTYPES = {torch.float32: QLORA_F32, torch.bfloat16: QLORA_BF16}
+
+
+def _adapter_rank(X: torch.Tensor, w: NF4Weight, nseg: int, A: torch.Tensor | None,
+                  B: torch.Tensor | None) -> tuple[int, int]:
+    """(M, r) after checking X, the weight's device and the adapters."""
+    if X.dim() != 2:
+        raise ValueError("X must be [M, K]")
+    _expect(X, "X", (X.shape[0], w.cols), torch.bfloat16, X.device)
+    if w.codes.device != X.device:
+        raise ValueError(f"the weight must be on {X.device}")
+    if (A is None) != (B is None):
+        raise ValueError("A and B are given together")
+    if A is None:
+        return X.shape[0], 0
+    if nseg < 1 or A.dim() != 2 or A.shape[0] % nseg:
+        raise ValueError("A must be [nseg * r, K]")
+    r = A.shape[0] // nseg
+    _expect(A, "A", (nseg * r, w.cols), torch.bfloat16, X.device)
+    _expect(B, "B", (w.rows, r), torch.bfloat16, X.device)
+    return X.shape[0], r
+
+
+def _adapter_grads(dA, dB, rows_a: int, w: NF4Weight, r: int, grad_dtype, device):
+    if grad_dtype not in _GRAD_DTYPES:
+        raise TypeError("grad_dtype must be torch.float32 or torch.bfloat16")
+    if r == 0:
+        return None, None
+    if dA is None:
+        dA = torch.empty(rows_a, w.cols, dtype=grad_dtype, device=device)
+    if dB is None:
+        dB = torch.empty(w.rows, r, dtype=grad_dtype, device=device)
+    _expect(dA, "dA", (rows_a, w.cols), grad_dtype, device)
+    _expect(dB, "dB", (w.rows, r), grad_dtype, device)
+    return dA, dB
+
+
+def qlora_dropout(X: torch.Tensor, dropout: Dropout, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Dropout of a dense bf16 or fp32 CUDA tensor: kept elements times the
+    inverse keep probability, dropped ones 0.  The gradient is the same call
+    on the output's gradient.  ``out`` may be X itself."""
+    if X.dtype not in _GRAD_DTYPES:
+        raise TypeError("X must be bf16 or fp32")
+    _expect(X, "X", X.shape, X.dtype, X.device)
+    if out is None:
+        out = torch.empty_like(X)
+    _expect(out, "out", X.shape, X.dtype, X.device)
+    with torch.cuda.device(X.device):
+        check(lib().qlora_dropout(_ptr(X), _GRAD_DTYPES[X.dtype], X.numel(), _drop_arg(dropout, X.device), _ptr(out),
+                                  _stream()), "qlora_dropout")
+    return out
+
+
+def qlora_fused_linear_dropout_workspace(M: int, w: NF4Weight, nseg: int, r: int, bwd: bool) -> int:
+    cw = w.c_struct()
+    return int(lib().qlora_fused_linear_dropout_workspace(M, ctypes.byref(cw), nseg, r, int(bwd)))
+
+
+def qlora_fused_linear_dropout_fwd(X: torch.Tensor, w: NF4Weight, nseg: int, A: torch.Tensor | None,
+                                   B: torch.Tensor | None, scale: float, dropout: Dropout | None,
+                                   Y: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
+    """qlora_fused_linear_fwd whose adapters read dropout(X); nseg 1 is the
+    plain linear."""
+    M, r = _adapter_rank(X, w, nseg, A, B)
+    if Y is None:
+        Y = torch.empty(M, w.rows, dtype=torch.bfloat16, device=X.device)
+    _expect(Y, "Y", (M, w.rows), torch.bfloat16, X.device)
+    wsb = _workspace(qlora_fused_linear_dropout_workspace(M, w, nseg, r, False), X.device, ws)
+    cw = w.c_struct()
+    with torch.cuda.device(X.device):
+        check(lib().qlora_fused_linear_dropout_fwd(_ptr(X), M, ctypes.byref(cw), nseg, _ptr(A), _ptr(B), r,
+                                                   float(scale), _drop_arg(dropout, X.device), _ptr(Y), _ptr(wsb),
+                                                   wsb.numel(), _stream()), "qlora_fused_linear_dropout_fwd")
+    return Y
+
+
+def qlora_fused_linear_dropout_bwd(dY: torch.Tensor, X: torch.Tensor, w: NF4Weight, nseg: int,
+                                   A: torch.Tensor | None, B: torch.Tensor | None, scale: float,
+                                   dropout: Dropout | None, dX: torch.Tensor | None = None,
+                                   dA: torch.Tensor | None = None, dB: torch.Tensor | None = None,
+                                   ws: torch.Tensor | None = None, want_dx: bool = True,
+                                   grad_dtype: torch.dtype = torch.float32):
+    """(dX, dA, dB) of qlora_fused_linear_dropout_fwd with the same dropout;
+    dA and dB in grad_dtype (fp32 or bf16)."""
+    M, r = _adapter_rank(X, w, nseg, A, B)
+    _expect(dY, "dY", (M, w.rows), torch.bfloat16, X.device)
+    if want_dx and dX is None:
+        dX = torch.empty(M, w.cols, dtype=torch.bfloat16, device=X.device)
+    _expect(dX, "dX", (M, w.cols), torch.bfloat16, X.device, optional=not want_dx)
+    dA, dB = _adapter_grads(dA, dB, nseg * r, w, r, grad_dtype, X.device)
+    wsb = _workspace(qlora_fused_linear_dropout_workspace(M, w, nseg, r, True), X.device, ws)
+    cw = w.c_struct()
+    with torch.cuda.device(X.device):
+        check(lib().qlora_fused_linear_dropout_bwd(
+            _ptr(dY), _ptr(X), M, ctypes.byref(cw), nseg, _ptr(A), _ptr(B), r, float(scale),
+            _drop_arg(dropout, X.device), _ptr(dX) if want_dx else None, _GRAD_DTYPES[grad_dtype], _ptr(dA), _ptr(dB),
+            _ptr(wsb), wsb.numel(), _stream()), "qlora_fused_linear_dropout_bwd")
+    return dX, dA, dB
+
+
+def qlora_gated_linear_workspace(M: int, w: NF4Weight, r: int, bwd: bool) -> int:
+    cw = w.c_struct()
+    return int(lib().qlora_gated_linear_workspace(M, ctypes.byref(cw), r, int(bwd)))
+
+
+def _act(act: str) -> int:
+    if act not in ACT_TYPES:
+        raise ValueError(f"act must be one of {sorted(ACT_TYPES)}")
+    return ACT_TYPES[act]
+
+
+def qlora_gated_linear_fwd(X: torch.Tensor, w: NF4Weight, A: torch.Tensor | None, B: torch.Tensor | None,
+                           scale: float, act: str = "silu", dropout: Dropout | None = None,
+                           H: torch.Tensor | None = None, GU: torch.Tensor | None = None, want_gu: bool = False,
+                           ws: torch.Tensor | None = None):
+    """(H, GU): H = act(g) u of the gated feed-forward block whose weight w
+    [2F, K] holds the gate rows, then the up rows; A [2r, K], B [2F, r].  GU
+    [M, 2F] = [g | u] for the backward, None unless want_gu or given."""
+    M, r = _adapter_rank(X, w, 2, A, B)
+    F = w.rows // 2
+    if H is None:
+        H = torch.empty(M, F, dtype=torch.bfloat16, device=X.device)
+    if want_gu and GU is None:
+        GU = torch.empty(M, w.rows, dtype=torch.bfloat16, device=X.device)
+    _expect(H, "H", (M, F), torch.bfloat16, X.device)
+    _expect(GU, "GU", (M, w.rows), torch.bfloat16, X.device, optional=True)
+    wsb = _workspace(qlora_gated_linear_workspace(M, w, r, False), X.device, ws)
+    cw = w.c_struct()
+    with torch.cuda.device(X.device):
+        check(lib().qlora_gated_linear_fwd(_ptr(X), M, ctypes.byref(cw), _ptr(A), _ptr(B), r, float(scale), _act(act),
+                                           _drop_arg(dropout, X.device), _ptr(H), _ptr(GU), _ptr(wsb), wsb.numel(),
+                                           _stream()), "qlora_gated_linear_fwd")
+    return H, GU
+
+
+def qlora_gated_linear_bwd(dH: torch.Tensor, X: torch.Tensor, GU: torch.Tensor, w: NF4Weight,
+                           A: torch.Tensor | None, B: torch.Tensor | None, scale: float, act: str = "silu",
+                           dropout: Dropout | None = None, dX: torch.Tensor | None = None,
+                           dA: torch.Tensor | None = None, dB: torch.Tensor | None = None,
+                           ws: torch.Tensor | None = None, want_dx: bool = True,
+                           grad_dtype: torch.dtype = torch.float32):
+    """(dX, dA, dB) of qlora_gated_linear_fwd from the gradient of H and the
+    kept GU, with the same dropout; dA and dB in grad_dtype."""
+    M, r = _adapter_rank(X, w, 2, A, B)
+    _expect(dH, "dH", (M, w.rows // 2), torch.bfloat16, X.device)
+    _expect(GU, "GU", (M, w.rows), torch.bfloat16, X.device)
+    if want_dx and dX is None:
+        dX = torch.empty(M, w.cols, dtype=torch.bfloat16, device=X.device)
+    _expect(dX, "dX", (M, w.cols), torch.bfloat16, X.device, optional=not want_dx)
+    dA, dB = _adapter_grads(dA, dB, 2 * r, w, r, grad_dtype, X.device)
+    wsb = _workspace(qlora_gated_linear_workspace(M, w, r, True), X.device, ws)
+    cw = w.c_struct()
+    with torch.cuda.device(X.device):
+        check(lib().qlora_gated_linear_bwd(
+            _ptr(dH), _ptr(X), _ptr(GU), M, ctypes.byref(cw), _ptr(A), _ptr(B), r, float(scale), _act(act),
+            _drop_arg(dropout, X.device), _ptr(dX) if want_dx else None, _GRAD_DTYPES[grad_dtype], _ptr(dA), _ptr(dB),
+            _ptr(wsb), wsb.numel(), _stream()), "qlora_gated_linear_bwd")
     return dX, dA, dB
 
 

@@ -1,0 +1,212 @@
+// dropout.cuh -- dropout from a counter-based generator, the keep mask
+// recomputed wherever it is needed and never stored.
+//
+// Generator: Philox-4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random
+// numbers: as easy as 1, 2, 3", 2011): ten rounds of two 32 x 32 -> 64 bit
+// products, key = the 64-bit seed, counter = (64-bit block number, 64-bit
+// offset).  One block gives the eight 15-bit numbers of eight consecutive
+// elements: word j holds element 2j's number in bits 0..14 and element
+// 2j + 1's in bits 16..30.  Element e = 8 block + i is kept if its number is
+// at least T = round(2^15 p), that is with probability exactly 1 - T / 2^15,
+// and kept elements are scaled by the exact inverse 2^15 / (2^15 - T).
+// Fifteen bits, because the halfword compare is then one add (a carry into
+// bit 15) and one byte permute for two elements; sixteen would take a compare
+// and a select for each.
+#pragma once
+
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace qlora {
+
+constexpr int kDropSteps = 32768;  // 2^15
+
+// A dropout in launch form.  thr == 0: no dropout.
+struct DropParams {
+    uint32_t rk[20];    // round keys: key words of rounds 0..9
+    uint32_t off_lo, off_hi;
+    const unsigned long long* off_dev;  // added to the offset when the kernel runs, or nullptr
+    uint32_t thr;       // T
+    uint32_t add;       // (2^15 - T) in both halves
+    float up;           // 2^15 / (2^15 - T)
+};
+
+inline void drop_params(DropParams* d, uint32_t thr, uint64_t seed, uint64_t offset, const uint64_t* offset_dev) {
+    uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
+    for (int i = 0; i < 10; ++i) {
+        d->rk[2 * i] = k0;
+        d->rk[2 * i + 1] = k1;
+        k0 += 0x9E3779B9u;  // Weyl constants of the paper
+        k1 += 0xBB67AE85u;
+    }
+    d->off_lo = (uint32_t)offset;
+    d->off_hi = (uint32_t)(offset >> 32);
+    d->off_dev = reinterpret_cast<const unsigned long long*>(offset_dev);
+    d->thr = thr;
+    d->add = (uint32_t)(kDropSteps - thr) * 0x10001u;
+    d->up = (float)((double)kDropSteps / (double)(kDropSteps - (int)thr));
+}
+
+// The offset words of a launch, with the device counter added.  The counter
+// may be written by an earlier kernel of the stream: call after pdl_wait.
+__device__ __forceinline__ uint2 drop_offset(const DropParams& d) {
+    unsigned long long o = ((unsigned long long)d.off_hi << 32) | d.off_lo;
+    if (d.off_dev) o += *d.off_dev;
+    return make_uint2((uint32_t)o, (uint32_t)(o >> 32));
+}
+
+// Keep masks of the eight elements of block `blk`: m[j] has 0xFFFF in the low
+// (high) half if element 2j (2j + 1) is kept, else 0.
+__device__ __forceinline__ void drop_mask8(const DropParams& d, uint2 off, uint64_t blk, uint32_t (&m)[4]) {
+    uint32_t c0 = (uint32_t)blk, c1 = (uint32_t)(blk >> 32), c2 = off.x, c3 = off.y;
+#pragma unroll
+    for (int i = 0; i < 10; ++i) {
+        const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
+        c0 = (uint32_t)(b >> 32) ^ c1 ^ d.rk[2 * i];
+        c1 = (uint32_t)b;
+        c2 = (uint32_t)(a >> 32) ^ c3 ^ d.rk[2 * i + 1];
+        c3 = (uint32_t)a;
+    }
+    const uint32_t w[4] = {c0, c1, c2, c3};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)  // bit 15 of each half: number >= T; replicated over the half
+        m[j] = prmt((w[j] & 0x7FFF7FFFu) + d.add, 0u, 0xBB99u);
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// ---------------------------------------------------------------------------
+// Y[e] = kept(e) ? X[e] * up : +0, elementwise (X and Y may be the same).
+// A dropped element gives +0 whatever X holds there.  bf16 products are
+// formed in fp32 and rounded once.
+// Bound by HBM: each element is read and written once.  A thread takes whole
+// eight-element blocks (16 bytes of bf16, 32 of fp32), UNROLL of them one
+// grid stride apart with all their loads issued first.
+// ---------------------------------------------------------------------------
+template <typename T, int UNROLL>
+__global__ void __launch_bounds__(256) k_dropout(const T* X, T* Y, int64_t n, const __grid_constant__ DropParams d) {
+    constexpr bool F32 = sizeof(T) == 4;
+    pdl_trigger();
+    pdl_wait();
+    const uint2 off = drop_offset(d);
+    const int64_t full = n >> 3;
+    const int64_t stride = (int64_t)gridDim.x * blockDim.x;
+    const int64_t t0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    const uint4* xv = reinterpret_cast<const uint4*>(X);
+    uint4* yv = reinterpret_cast<uint4*>(Y);
+    for (int64_t b0 = t0; b0 < full; b0 += stride * UNROLL) {
+        uint4 v[UNROLL][F32 ? 2 : 1];
+#pragma unroll
+        for (int q = 0; q < UNROLL; ++q) {
+            const int64_t b = b0 + q * stride;
+            if (b < full) {
+                if (F32) {
+                    v[q][0] = xv[2 * b];
+                    v[q][F32 ? 1 : 0] = xv[2 * b + 1];
+                } else {
+                    v[q][0] = xv[b];
+                }
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < UNROLL; ++q) {
+            const int64_t b = b0 + q * stride;
+            if (b >= full) break;
+            uint32_t m[4] = {~0u, ~0u, ~0u, ~0u};
+            if (d.thr) drop_mask8(d, off, (uint64_t)b, m);
+            if (F32) {
+                uint32_t w[8] = {v[q][0].x, v[q][0].y, v[q][0].z, v[q][0].w,
+                                 v[q][F32 ? 1 : 0].x, v[q][F32 ? 1 : 0].y, v[q][F32 ? 1 : 0].z, v[q][F32 ? 1 : 0].w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t keep = (i & 1) ? prmt(m[i >> 1], 0u, 0x3232u) : prmt(m[i >> 1], 0u, 0x1010u);
+                    w[i] = __float_as_uint(__fmul_rn(__uint_as_float(w[i]), d.up)) & keep;
+                }
+                yv[2 * b] = make_uint4(w[0], w[1], w[2], w[3]);
+                yv[2 * b + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+            } else {
+                uint32_t w[4] = {v[q][0].x, v[q][0].y, v[q][0].z, v[q][0].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    w[j] = pack_bf16x2(__fmul_rn(bf16_lo(w[j]), d.up), __fmul_rn(bf16_hi(w[j]), d.up)) & m[j];
+                yv[b] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+    }
+    // the last, partial block
+    const int tail = (int)(n & 7);
+    if (tail && t0 == 0) {
+        uint32_t m[4] = {~0u, ~0u, ~0u, ~0u};
+        if (d.thr) drop_mask8(d, off, (uint64_t)full, m);
+        for (int i = 0; i < tail; ++i) {
+            const int64_t e = 8 * full + i;
+            const bool keep = (m[i >> 1] >> (16 * (i & 1))) & 1u;
+            if (F32) {
+                const float x = reinterpret_cast<const float*>(X)[e];
+                reinterpret_cast<float*>(Y)[e] = keep ? __fmul_rn(x, d.up) : 0.0f;
+            } else {
+                const float x = bf16_lo(reinterpret_cast<const uint16_t*>(X)[e]);
+                reinterpret_cast<uint16_t*>(Y)[e] =
+                    keep ? (uint16_t)(pack_bf16x2(__fmul_rn(x, d.up), 0.0f) & 0xFFFFu) : (uint16_t)0;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Adapter dropout of the linear: masked copy of X for the adapter GEMMs, and
+// the masked adapter term of dX.
+// ---------------------------------------------------------------------------
+// Xd = X where kept, else +0 (unscaled: the factor goes into the adapter's
+// scale, so that the masked bf16 values stay exact); n8 blocks of eight.
+__global__ void __launch_bounds__(256) k_drop_mask(const uint4* X, uint4* Xd, int64_t n8,
+                                                   const __grid_constant__ DropParams d) {
+    pdl_trigger();
+    pdl_wait();
+    const uint2 off = drop_offset(d);
+    for (int64_t b = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; b < n8; b += (int64_t)gridDim.x * blockDim.x) {
+        uint32_t m[4];
+        drop_mask8(d, off, (uint64_t)b, m);
+        const uint4 v = X[b];
+        Xd[b] = make_uint4(v.x & m[0], v.y & m[1], v.z & m[2], v.w & m[3]);
+    }
+}
+
+// dX[m][k] += kept(m K + k) * sum_j G[m][j] A[j][k], eight columns a thread.
+__global__ void __launch_bounds__(256) k_lora_dx_masked(uint4* dX, const uint16_t* G, const uint16_t* A, int64_t M,
+                                                        int64_t K, int rt, const __grid_constant__ DropParams d) {
+    pdl_trigger();
+    pdl_wait();
+    const uint2 off = drop_offset(d);
+    const int64_t k8 = K / 8;
+    for (int64_t b = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; b < M * k8;
+         b += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t m = b / k8, c = b - m * k8;
+        float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int j = 0; j < rt; ++j) {
+            const float g = bf16_lo(G[m * rt + j]);
+            const uint4 a = *reinterpret_cast<const uint4*>(A + (int64_t)j * K + c * 8);
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                acc[2 * q] = fmaf(g, bf16_lo(w[q]), acc[2 * q]);
+                acc[2 * q + 1] = fmaf(g, bf16_hi(w[q]), acc[2 * q + 1]);
+            }
+        }
+        uint32_t mk[4];
+        drop_mask8(d, off, (uint64_t)b, mk);
+        const uint4 v = dX[b];
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t sum = pack_bf16x2(bf16_lo(x[q]) + acc[2 * q], bf16_hi(x[q]) + acc[2 * q + 1]);
+            o[q] = (sum & mk[q]) | (x[q] & ~mk[q]);
+        }
+        dX[b] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+}  // namespace qlora

@@ -73,12 +73,18 @@ struct LinearArgs {
     const qlora_nf4_weight* w;
     int nseg;
     int64_t seg_rows;
+    // adapter dropout (null: none), and what the adapter reads in place of X
+    // then; scale already holds the factor of the kept elements
+    const struct DropParams* drop;
+    const void* Xd;
+    int grad_bf16;  // dA and dB in bf16 instead of fp32
     int rt() const { return r * nseg; }  // columns of sU and sG
+    const void* adapter_in(const void* X) const { return Xd ? Xd : X; }
 };
 qlora_status linear_fwd_impl(const void* X, const LinearArgs& a, const void* A, const void* B,
                              void* Y, void* ws, size_t ws_bytes, cudaStream_t s);
 qlora_status linear_bwd_impl(const void* dY, const void* X, const LinearArgs& a, const void* A,
-                             const void* B, void* dX, float* dA, float* dB, void* ws,
+                             const void* B, void* dX, void* dA, void* dB, void* ws,
                              size_t ws_bytes, cudaStream_t s);
 size_t linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int r, int bwd);
 

@@ -20,6 +20,8 @@
 #include <mutex>
 #include <utility>
 
+#include "dropout.cuh"
+#include "gated.cuh"
 #include "gemm.cuh"
 #include "gemm_pair.cuh"
 #include "skinny.cuh"
@@ -455,7 +457,7 @@ inline bool map_codes(CUtensorMap* m, const qlora_nf4_weight& w, uint32_t box_by
 // (A = [A_0; A_1; ...] of a fused projection: every adapter's sU in one pass over X)
 inline bool desc_sU(SkinnyDesc* d, const void* X, const LinearArgs& a, const void* A, void* sU) {
     memset(d, 0, sizeof(*d));
-    if (!map_bf16(&d->tA, X, a.K, a.M, 128)) return false;
+    if (!map_bf16(&d->tA, a.adapter_in(X), a.K, a.M, 128)) return false;
     if (!map_bf16(&d->tB, A, a.K, a.rt(), lora_bn(a.rt()))) return false;
     d->rows = (int)a.M;
     d->ksteps = (int)(a.K / 64);
@@ -711,19 +713,19 @@ inline bool desc_sG(SkinnyDesc* d, const CUtensorMap& tdY, const LinearArgs& a, 
 // dA^T [K][r] = X^T sG : Aop = X viewed [k][m] (MN-major), Bop = sG viewed [j][m] (MN-major)
 // dB [N][r] = dY^T sU : Aop = dY viewed [n][m] (MN-major), Bop = sU viewed [j][m]
 inline bool desc_dA_dB(SkinnyDesc* d, const void* dY, const void* X, const LinearArgs& a, const LinearWs& L,
-                       float* dA, float* dB) {
+                       void* dA, void* dB) {
     memset(d, 0, 2 * sizeof(*d));
-    if (!map_bf16(&d[0].tA, X, a.K, a.M, 64)) return false;
+    if (!map_bf16(&d[0].tA, a.adapter_in(X), a.K, a.M, 64)) return false;
     if (!map_bf16(&d[0].tB, L.sG, a.rt(), a.M, 64)) return false;
     d[0].rows = (int)a.K;
-    d[0].out_mode = SK_OUT_F32_T;
+    d[0].out_mode = a.grad_bf16 ? SK_OUT_BF16_T : SK_OUT_F32_T;
     d[0].out = dA;
     d[0].out_ld = a.K;
     d[0].r = a.rt();
     if (!map_bf16(&d[1].tA, dY, a.N, a.M, 64)) return false;
     if (!map_bf16(&d[1].tB, L.sU, a.rt(), a.M, 64)) return false;
     d[1].rows = (int)a.N;
-    d[1].out_mode = SK_OUT_F32;
+    d[1].out_mode = a.grad_bf16 ? SK_OUT_BF16 : SK_OUT_F32;
     d[1].out = dB;
     d[1].out_ld = a.r;
     d[1].r = a.r;
@@ -751,7 +753,8 @@ inline qlora_status launch_dx_gemm(const void* A, void* dX, const LinearArgs& a,
     p.tmA = tdY;
     p.tmB = tdY;
     if (!map_codes(&p.tmCodes, w, 128, 64)) return QLORA_ERR_CUDA;
-    if (a.r > 0) {
+    const bool lora = a.r > 0 && !a.drop;  // with dropout the adapter term is masked and added apart
+    if (lora) {
         if (!map_bf16(&p.tmA2, L.sG, a.rt(), a.M, 128)) return QLORA_ERR_CUDA;
         if (!map_bf16(&p.tmB2, A, a.K, a.rt(), 64)) return QLORA_ERR_CUDA;
     } else {
@@ -764,7 +767,7 @@ inline qlora_status launch_dx_gemm(const void* A, void* dX, const LinearArgs& a,
     p.dq_rows = (int)a.N;
     p.dq_kbs = (int)(a.K / 64);
     p.ks_main = ceil_div(a.N, 64);
-    p.ks_lora = a.r > 0 ? ceil_div(a.rt(), 64) : 0;
+    p.ks_lora = lora ? ceil_div(a.rt(), 64) : 0;
     p.ks_per_split = p.ks_main;
     p.rows = (int)a.M;
     p.cols = (int)a.K;
@@ -786,6 +789,34 @@ inline qlora_status launch_dx_gemm(const void* A, void* dX, const LinearArgs& a,
     return QLORA_OK;
 }
 
+// Grid of an elementwise kernel of 256 threads over n items.
+inline unsigned elementwise_grid(int64_t n) {
+    return (unsigned)std::max<int64_t>(1, std::min<int64_t>((n + 255) / 256, (int64_t)sm_count() * 8));
+}
+
+// Y = dropout(X), n elements: four blocks of eight in flight a thread for
+// bf16 (64 bytes), two for fp32 (64 bytes).
+inline cudaError_t launch_dropout(const void* X, bool is_bf16, int64_t n, const DropParams& d, void* Y,
+                                  cudaStream_t s) {
+    note_launch();
+    const unsigned grid = elementwise_grid(n / 8 + 1);
+    if (is_bf16)
+        return launch_pdl(k_dropout<uint16_t, 4>, dim3(grid), dim3(256), 0, s, 0, static_cast<const uint16_t*>(X),
+                          static_cast<uint16_t*>(Y), n, d);
+    return launch_pdl(k_dropout<float, 2>, dim3(grid), dim3(256), 0, s, 0, static_cast<const float*>(X),
+                      static_cast<float*>(Y), n, d);
+}
+
+// dX += keep * (sG A)
+inline qlora_status launch_lora_dx_masked(const void* A, void* dX, const LinearArgs& a, const LinearWs& L,
+                                          cudaStream_t s) {
+    note_launch();
+    const cudaError_t e = launch_pdl(k_lora_dx_masked, dim3(elementwise_grid(a.M * a.K / 8)), dim3(256), 0, s, 0,
+                                     static_cast<uint4*>(dX), (const uint16_t*)L.sG, static_cast<const uint16_t*>(A),
+                                     a.M, a.K, a.rt(), *a.drop);
+    return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+}
+
 // The backward forks its adapter GEMMs onto the side stream when the dX GEMM
 // runs on the CTA-pair kernel, one pair per tile.
 inline bool side_fork_ok() { return large_m_schedule() == SCHED_PAIR; }
@@ -798,7 +829,7 @@ inline bool side_fork_ok() { return large_m_schedule() == SCHED_PAIR; }
 //   side: wait for sG -> sU -> dA, dB (one CTA per tile each), on the SMs the
 //         GEMM leaves free
 inline qlora_status linear_bwd_forked(const void* dY, const void* X, const LinearArgs& a, const void* A,
-                                      const void* B, void* dX, float* dA, float* dB, const LinearWs& L,
+                                      const void* B, void* dX, void* dA, void* dB, const LinearWs& L,
                                       const CUtensorMap& tdY, const SideStream& side, cudaStream_t s) {
     SkinnyDesc dg;
     if (!desc_sG(&dg, tdY, a, B, L.sG)) return QLORA_ERR_CUDA;
@@ -807,7 +838,8 @@ inline qlora_status linear_bwd_forked(const void* dY, const void* X, const Linea
     if (cudaEventRecord(side.fork, s) != cudaSuccess) return QLORA_ERR_CUDA;
     if (cudaStreamWaitEvent(side.st, side.fork, 0) != cudaSuccess) return QLORA_ERR_CUDA;
     // from here on the side stream is joined back whatever happens
-    st = launch_dx_gemm(A, dX, a, L, tdY, 1, s);
+    st = launch_dx_gemm(A, dX, a, L, tdY, a.drop ? 0 : 1, s);
+    if (st == QLORA_OK && a.drop) st = launch_lora_dx_masked(A, dX, a, L, s);
     // sU, dA and dB in one persistent launch over every SM: the CTAs that
     // find an SM beside the GEMM take tiles from the shared counter while it
     // runs, the rest start as it ends.  sU tiles (inputs only) start at once,
@@ -823,7 +855,7 @@ inline qlora_status linear_bwd_forked(const void* dY, const void* X, const Linea
 }
 
 inline qlora_status linear_bwd_impl(const void* dY, const void* X, const LinearArgs& a,
-                                    const void* A, const void* B, void* dX, float* dA, float* dB,
+                                    const void* A, const void* B, void* dX, void* dA, void* dB,
                                     void* ws, size_t ws_bytes, cudaStream_t s) {
     (void)ws_bytes;
     const qlora_nf4_weight& w = *a.w;
@@ -831,9 +863,11 @@ inline qlora_status linear_bwd_impl(const void* dY, const void* X, const LinearA
     if (a.M == 0) {
         if (a.r > 0) {
             note_launch();
-            k_fill_zero_f32<<<64, 256, 0, s>>>(dA, (int64_t)a.rt() * a.K);
+            // (both counts are even: bf16 zeros as pairs)
+            const int h = a.grad_bf16 ? 2 : 1;
+            k_fill_zero_f32<<<64, 256, 0, s>>>(static_cast<float*>(dA), (int64_t)a.rt() * a.K / h);
             note_launch();
-            k_fill_zero_f32<<<64, 256, 0, s>>>(dB, a.N * a.r);
+            k_fill_zero_f32<<<64, 256, 0, s>>>(static_cast<float*>(dB), a.N * a.r / h);
             if (cudaGetLastError() != cudaSuccess) return QLORA_ERR_CUDA;
         }
         return QLORA_OK;
@@ -861,6 +895,7 @@ inline qlora_status linear_bwd_impl(const void* dY, const void* X, const LinearA
     }
     if (dX) {
         qlora_status st = launch_dx_gemm(A, dX, a, L, tdY, 0, s);
+        if (st == QLORA_OK && a.drop) st = launch_lora_dx_masked(A, dX, a, L, s);
         if (st != QLORA_OK) return st;
     }
     if (a.r > 0) {
@@ -871,6 +906,89 @@ inline qlora_status linear_bwd_impl(const void* dY, const void* X, const LinearA
         if (st != QLORA_OK) return st;
     }
     return QLORA_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Adapter dropout and the gated feed-forward on the linear's forward and
+// backward.  Workspace: the linear's, then the masked X (dropout), then the
+// pre-activations [M, 2F] the caller does not keep (gated forward) or their
+// gradient (gated backward).
+// ---------------------------------------------------------------------------
+struct BlockWs {
+    void* linear;
+    size_t linear_bytes;
+    void* Xd;
+    uint16_t* gu;
+    size_t bytes;
+};
+
+inline BlockWs carve_block_ws(void* ws, int64_t M, int64_t N, int64_t K, int rt, int bwd, int gated) {
+    BlockWs b;
+    b.linear_bytes = linear_workspace_bytes(M, N, K, rt, bwd);
+    WsCarve c{static_cast<char*>(ws), 0};
+    b.linear = c.take(b.linear_bytes);
+    b.Xd = rt > 0 ? c.take((size_t)M * K * 2) : nullptr;
+    b.gu = gated ? static_cast<uint16_t*>(c.take((size_t)M * N * 2)) : nullptr;
+    b.bytes = c.used;
+    return b;
+}
+
+// The adapter's input under dropout: X where kept, else 0.
+inline qlora_status mask_input(const void* X, LinearArgs& a, const BlockWs& b, cudaStream_t s) {
+    if (!a.drop) return QLORA_OK;
+    a.Xd = b.Xd;
+    note_launch();
+    const int64_t n8 = a.M * a.K / 8;
+    const cudaError_t e = launch_pdl(k_drop_mask, dim3(elementwise_grid(n8)), dim3(256), 0, s, 0,
+                                     static_cast<const uint4*>(X), static_cast<uint4*>(b.Xd), n8, *a.drop);
+    return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+}
+
+inline qlora_status dropout_fwd_impl(const void* X, LinearArgs a, const void* A, const void* B, void* Y, void* ws,
+                                     cudaStream_t s) {
+    const BlockWs b = carve_block_ws(ws, a.M, a.N, a.K, a.rt(), 0, 0);
+    qlora_status st = mask_input(X, a, b, s);
+    if (st != QLORA_OK) return st;
+    return linear_fwd_impl(X, a, A, B, Y, b.linear, b.linear_bytes, s);
+}
+
+inline qlora_status dropout_bwd_impl(const void* dY, const void* X, LinearArgs a, const void* A, const void* B,
+                                     void* dX, void* dA, void* dB, void* ws, cudaStream_t s) {
+    const BlockWs b = carve_block_ws(ws, a.M, a.N, a.K, a.rt(), 1, 0);
+    if (a.M > 0) {
+        qlora_status st = mask_input(X, a, b, s);
+        if (st != QLORA_OK) return st;
+    }
+    return linear_bwd_impl(dY, X, a, A, B, dX, dA, dB, b.linear, b.linear_bytes, s);
+}
+
+inline qlora_status gated_fwd_impl(const void* X, LinearArgs a, const void* A, const void* B, int act, void* H,
+                                   void* GU, void* ws, cudaStream_t s) {
+    const BlockWs b = carve_block_ws(ws, a.M, a.N, a.K, a.rt(), 0, 1);
+    qlora_status st = mask_input(X, a, b, s);
+    if (st != QLORA_OK) return st;
+    uint16_t* gu = GU ? static_cast<uint16_t*>(GU) : b.gu;
+    st = linear_fwd_impl(X, a, A, B, gu, b.linear, b.linear_bytes, s);
+    if (st != QLORA_OK) return st;
+    note_launch();
+    const cudaError_t e = launch_pdl(k_gated_act, dim3(elementwise_grid(a.M * a.seg_rows / 8)), dim3(256), 0, s, 0,
+                                     (const uint16_t*)gu, static_cast<uint16_t*>(H), a.M, a.seg_rows, act);
+    return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+}
+
+inline qlora_status gated_bwd_impl(const void* dH, const void* X, const void* GU, LinearArgs a, const void* A,
+                                   const void* B, int act, void* dX, void* dA, void* dB, void* ws, cudaStream_t s) {
+    const BlockWs b = carve_block_ws(ws, a.M, a.N, a.K, a.rt(), 1, 1);
+    if (a.M > 0) {
+        qlora_status st = mask_input(X, a, b, s);
+        if (st != QLORA_OK) return st;
+        note_launch();
+        const cudaError_t e = launch_pdl(k_gated_grad, dim3(elementwise_grid(a.M * a.seg_rows / 8)), dim3(256), 0, s,
+                                         0, static_cast<const uint16_t*>(dH), static_cast<const uint16_t*>(GU), b.gu,
+                                         a.M, a.seg_rows, act);
+        if (e != cudaSuccess) return QLORA_ERR_CUDA;
+    }
+    return linear_bwd_impl(b.gu, X, a, A, B, dX, dA, dB, b.linear, b.linear_bytes, s);
 }
 
 }  // namespace qlora

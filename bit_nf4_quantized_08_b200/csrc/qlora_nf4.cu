@@ -262,6 +262,39 @@ static qlora_status check_fused(int64_t M, const qlora_nf4_weight* w, int32_t ns
     return QLORA_OK;
 }
 
+// T = round(2^15 p) of a dropout, and its launch form.  A null config, or a
+// probability that rounds to 0, is no dropout (thr 0).
+static qlora_status check_dropout(const qlora_dropout_config* c, DropParams* d) {
+    memset(d, 0, sizeof(*d));
+    d->up = 1.0f;
+    if (!c) return QLORA_OK;
+    if (!(c->p >= 0.0f && c->p < 1.0f)) return QLORA_ERR_INVALID_ARG;  // also NaN
+    if (!aligned(c->offset_dev, 8)) return QLORA_ERR_INVALID_ARG;
+    const int thr = (int)floor((double)c->p * kDropSteps + 0.5);
+    if (thr >= kDropSteps) return QLORA_ERR_INVALID_ARG;  // nothing would be kept
+    if (thr > 0) drop_params(d, (uint32_t)thr, c->seed, c->offset, c->offset_dev);
+    return QLORA_OK;
+}
+
+// Adapter scale under dropout: the kept elements' factor, rounded once.
+static float dropped_scale(float scale, const DropParams& d) {
+    return d.thr ? (float)((double)scale * kDropSteps / (double)(kDropSteps - (int)d.thr)) : scale;
+}
+
+// The gated feed-forward's weight: the gate rows, then the up rows.
+static qlora_status check_gated(int64_t M, const qlora_nf4_weight* w, int32_t r, int32_t act) {
+    const qlora_status st = check_fused(M, w, 2, r);
+    if (st != QLORA_OK) return st;
+    return act == QLORA_ACT_SILU || act == QLORA_ACT_GELU_TANH ? QLORA_OK : QLORA_ERR_INVALID_ARG;
+}
+
+static bool adapter_ok(const void* A, const void* B, int32_t r) {
+    return r == 0 || (A && aligned(A, 16) && B && aligned(B, 16));
+}
+static bool grads_ok(const void* dA, const void* dB, int32_t r) {
+    return r == 0 || (dA && aligned(dA, 16) && dB && aligned(dB, 16));
+}
+
 }  // namespace qlora
 
 using namespace qlora;
@@ -374,7 +407,7 @@ qlora_status qlora_fused_linear_fwd(const void* X, int64_t M, const qlora_nf4_we
     if (r > 0 && (!A || !aligned(A, 16) || !B || !aligned(B, 16))) return QLORA_ERR_INVALID_ARG;
     const size_t need = linear_workspace_bytes(M, w->rows, w->cols, r * nseg, 0);
     if (!ws || !aligned(ws, 16) || ws_bytes < need) return QLORA_ERR_INVALID_ARG;
-    LinearArgs a{M, w->rows, w->cols, r, scale, w, nseg, w->rows / nseg};
+    LinearArgs a{M, w->rows, w->cols, r, scale, w, nseg, w->rows / nseg, nullptr, nullptr, 0};
     return linear_fwd_impl(X, a, A, B, Y, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -400,7 +433,7 @@ qlora_status qlora_fused_linear_bwd(const void* dY, const void* X, int64_t M, co
     }
     const size_t need = linear_workspace_bytes(M, w->rows, w->cols, r * nseg, 1);
     if (!ws || !aligned(ws, 16) || ws_bytes < need) return QLORA_ERR_INVALID_ARG;
-    LinearArgs a{M, w->rows, w->cols, r, scale, w, nseg, w->rows / nseg};
+    LinearArgs a{M, w->rows, w->cols, r, scale, w, nseg, w->rows / nseg, nullptr, nullptr, 0};
     return linear_bwd_impl(dY, X, a, A, B, dX, dA, dB, ws, ws_bytes,
                            reinterpret_cast<cudaStream_t>(stream));
 }
@@ -410,6 +443,109 @@ qlora_status qlora_linear_bwd(const void* dY, const void* X, int64_t M, const ql
                               float* dA, float* dB, void* ws, size_t ws_bytes,
                               qlora_stream_t stream) {
     return qlora_fused_linear_bwd(dY, X, M, w, 1, A, B, r, scale, dX, dA, dB, ws, ws_bytes, stream);
+}
+
+qlora_status qlora_dropout(const void* X, qlora_dtype dtype, int64_t n, const qlora_dropout_config* drop, void* Y,
+                           qlora_stream_t stream) {
+    NvtxRange nvtx_range("qlora_dropout");
+    DropParams d;
+    if (!drop || n < 0 || (dtype != QLORA_F32 && dtype != QLORA_BF16)) return QLORA_ERR_INVALID_ARG;
+    const qlora_status st = check_dropout(drop, &d);
+    if (st != QLORA_OK || n == 0) return st;
+    if (!X || !aligned(X, 16) || !Y || !aligned(Y, 16)) return QLORA_ERR_INVALID_ARG;
+    return launch_dropout(X, dtype == QLORA_BF16, n, d, Y, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? QLORA_OK
+               : QLORA_ERR_CUDA;
+}
+
+size_t qlora_fused_linear_dropout_workspace(int64_t M, const qlora_nf4_weight* w, int32_t nseg, int32_t r,
+                                            int32_t bwd) {
+    if (check_fused(M, w, nseg, r) != QLORA_OK) return 0;
+    return carve_block_ws(nullptr, M, w->rows, w->cols, r * nseg, bwd ? 1 : 0, 0).bytes;
+}
+
+qlora_status qlora_fused_linear_dropout_fwd(const void* X, int64_t M, const qlora_nf4_weight* w, int32_t nseg,
+                                            const void* A, const void* B, int32_t r, float scale,
+                                            const qlora_dropout_config* drop, void* Y, void* ws, size_t ws_bytes,
+                                            qlora_stream_t stream) {
+    NvtxRange nvtx_range("qlora_fused_linear_dropout_fwd");
+    qlora_status st = check_fused(M, w, nseg, r);
+    if (st != QLORA_OK) return st;
+    DropParams d;
+    st = check_dropout(drop, &d);
+    if (st != QLORA_OK || M == 0) return st;
+    if (!X || !aligned(X, 16) || !Y || !aligned(Y, 16) || !adapter_ok(A, B, r)) return QLORA_ERR_INVALID_ARG;
+    const size_t need = carve_block_ws(nullptr, M, w->rows, w->cols, r * nseg, 0, 0).bytes;
+    if (!ws || !aligned(ws, 16) || ws_bytes < need) return QLORA_ERR_INVALID_ARG;
+    LinearArgs a{M, w->rows, w->cols, r, dropped_scale(scale, d), w, nseg, w->rows / nseg,
+                 d.thr && r > 0 ? &d : nullptr, nullptr, 0};
+    return dropout_fwd_impl(X, a, A, B, Y, ws, reinterpret_cast<cudaStream_t>(stream));
+}
+
+qlora_status qlora_fused_linear_dropout_bwd(const void* dY, const void* X, int64_t M, const qlora_nf4_weight* w,
+                                            int32_t nseg, const void* A, const void* B, int32_t r, float scale,
+                                            const qlora_dropout_config* drop, void* dX, qlora_dtype grad_dtype,
+                                            void* dA, void* dB, void* ws, size_t ws_bytes, qlora_stream_t stream) {
+    NvtxRange nvtx_range("qlora_fused_linear_dropout_bwd");
+    qlora_status st = check_fused(M, w, nseg, r);
+    if (st != QLORA_OK) return st;
+    DropParams d;
+    st = check_dropout(drop, &d);
+    if (st != QLORA_OK) return st;
+    if (grad_dtype != QLORA_F32 && grad_dtype != QLORA_BF16) return QLORA_ERR_INVALID_ARG;
+    if (!adapter_ok(A, B, r) || !grads_ok(dA, dB, r)) return QLORA_ERR_INVALID_ARG;
+    if (M > 0 && (!dY || !aligned(dY, 16) || !X || !aligned(X, 16) || !aligned(dX, 16))) return QLORA_ERR_INVALID_ARG;
+    const size_t need = carve_block_ws(nullptr, M, w->rows, w->cols, r * nseg, 1, 0).bytes;
+    if (!ws || !aligned(ws, 16) || ws_bytes < need) return QLORA_ERR_INVALID_ARG;
+    LinearArgs a{M, w->rows, w->cols, r, dropped_scale(scale, d), w, nseg, w->rows / nseg,
+                 d.thr && r > 0 ? &d : nullptr, nullptr, grad_dtype == QLORA_BF16};
+    return dropout_bwd_impl(dY, X, a, A, B, dX, dA, dB, ws, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t qlora_gated_linear_workspace(int64_t M, const qlora_nf4_weight* w, int32_t r, int32_t bwd) {
+    if (check_fused(M, w, 2, r) != QLORA_OK) return 0;
+    return carve_block_ws(nullptr, M, w->rows, w->cols, 2 * r, bwd ? 1 : 0, 1).bytes;
+}
+
+qlora_status qlora_gated_linear_fwd(const void* X, int64_t M, const qlora_nf4_weight* w, const void* A,
+                                    const void* B, int32_t r, float scale, int32_t act,
+                                    const qlora_dropout_config* drop, void* H, void* GU, void* ws, size_t ws_bytes,
+                                    qlora_stream_t stream) {
+    NvtxRange nvtx_range("qlora_gated_linear_fwd");
+    qlora_status st = check_gated(M, w, r, act);
+    if (st != QLORA_OK) return st;
+    DropParams d;
+    st = check_dropout(drop, &d);
+    if (st != QLORA_OK || M == 0) return st;
+    if (!X || !aligned(X, 16) || !H || !aligned(H, 16) || !aligned(GU, 16) || !adapter_ok(A, B, r))
+        return QLORA_ERR_INVALID_ARG;
+    const size_t need = carve_block_ws(nullptr, M, w->rows, w->cols, 2 * r, 0, 1).bytes;
+    if (!ws || !aligned(ws, 16) || ws_bytes < need) return QLORA_ERR_INVALID_ARG;
+    LinearArgs a{M, w->rows, w->cols, r, dropped_scale(scale, d), w, 2, w->rows / 2,
+                 d.thr && r > 0 ? &d : nullptr, nullptr, 0};
+    return gated_fwd_impl(X, a, A, B, act, H, GU, ws, reinterpret_cast<cudaStream_t>(stream));
+}
+
+qlora_status qlora_gated_linear_bwd(const void* dH, const void* X, const void* GU, int64_t M,
+                                    const qlora_nf4_weight* w, const void* A, const void* B, int32_t r, float scale,
+                                    int32_t act, const qlora_dropout_config* drop, void* dX, qlora_dtype grad_dtype,
+                                    void* dA, void* dB, void* ws, size_t ws_bytes, qlora_stream_t stream) {
+    NvtxRange nvtx_range("qlora_gated_linear_bwd");
+    qlora_status st = check_gated(M, w, r, act);
+    if (st != QLORA_OK) return st;
+    DropParams d;
+    st = check_dropout(drop, &d);
+    if (st != QLORA_OK) return st;
+    if (grad_dtype != QLORA_F32 && grad_dtype != QLORA_BF16) return QLORA_ERR_INVALID_ARG;
+    if (!adapter_ok(A, B, r) || !grads_ok(dA, dB, r)) return QLORA_ERR_INVALID_ARG;
+    if (M > 0 && (!dH || !aligned(dH, 16) || !X || !aligned(X, 16) || !GU || !aligned(GU, 16) || !aligned(dX, 16)))
+        return QLORA_ERR_INVALID_ARG;
+    const size_t need = carve_block_ws(nullptr, M, w->rows, w->cols, 2 * r, 1, 1).bytes;
+    if (!ws || !aligned(ws, 16) || ws_bytes < need) return QLORA_ERR_INVALID_ARG;
+    if (!dX && r == 0) return QLORA_OK;  // nothing asked for
+    LinearArgs a{M, w->rows, w->cols, r, dropped_scale(scale, d), w, 2, w->rows / 2,
+                 d.thr && r > 0 ? &d : nullptr, nullptr, grad_dtype == QLORA_BF16};
+    return gated_bwd_impl(dH, X, GU, a, A, B, act, dX, dA, dB, ws, reinterpret_cast<cudaStream_t>(stream));
 }
 
 qlora_status qlora_lora_merge(const qlora_nf4_weight* w, const void* A, const void* B, int32_t r,

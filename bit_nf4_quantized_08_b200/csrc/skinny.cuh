@@ -22,7 +22,8 @@
 
 namespace qlora {
 
-enum { SK_OUT_BF16 = 0, SK_OUT_F32 = 1, SK_OUT_F32_T = 2 };
+// output: row-major bf16 or fp32, or transposed (out[j][i]) fp32 or bf16
+enum { SK_OUT_BF16 = 0, SK_OUT_F32 = 1, SK_OUT_F32_T = 2, SK_OUT_BF16_T = 3 };
 
 struct SkinnyProblem {
     CUtensorMap tmA, tmB;
@@ -290,14 +291,19 @@ __global__ void __launch_bounds__(SkinnyShape<BN>::THREADS, 1) k_skinny(const __
         const int nrows = got ? max(0, min(rows_per, min(128, P.rows - m0) - r0)) : 0;
         const float* red = reinterpret_cast<const float*>(gbase + S::RED_OFF);
         constexpr int LD = S::PART_LD;
-        if (P.out_mode == SK_OUT_F32_T) {
+        if (P.out_mode == SK_OUT_F32_T || P.out_mode == SK_OUT_BF16_T) {
             // out[j][m0 + r0 + rr]: consecutive threads take consecutive rows
             float* out = static_cast<float*>(P.out);
+            uint16_t* out_h = static_cast<uint16_t*>(P.out);
             for (int e = t; e < nrows * P.r; e += 128) {
                 const int j = e / nrows, rr = e - j * nrows;
                 float acc = red[rr * LD + j];
                 for (int zz = 1; zz < cs; ++zz) acc = __fadd_rn(acc, red[(zz * rows_per + rr) * LD + j]);
-                out[(int64_t)j * P.out_ld + m0 + r0 + rr] = __fmul_rn(acc, P.scale);
+                const int64_t o = (int64_t)j * P.out_ld + m0 + r0 + rr;
+                if (P.out_mode == SK_OUT_F32_T)
+                    out[o] = __fmul_rn(acc, P.scale);
+                else
+                    out_h[o] = (uint16_t)(pack_bf16x2(__fmul_rn(acc, P.scale), 0.0f) & 0xFFFFu);
             }
         } else {
             // four consecutive columns per thread (r % 8 == 0)
@@ -589,6 +595,13 @@ __global__ void __launch_bounds__(StreamShape<BN>::THREADS, 1) k_lora_stream(con
                     for (int q = 0; q < 32; ++q)
                         if (c0 + q < P.r)
                             out[(int64_t)(c0 + q) * P.out_ld + m] = __fmul_rn(__uint_as_float(v[q]), P.scale);
+                } else if (P.out_mode == SK_OUT_BF16_T) {
+                    uint16_t* out = static_cast<uint16_t*>(P.out);
+#pragma unroll
+                    for (int q = 0; q < 32; ++q)
+                        if (c0 + q < P.r)
+                            out[(int64_t)(c0 + q) * P.out_ld + m] =
+                                (uint16_t)(pack_bf16x2(__fmul_rn(__uint_as_float(v[q]), P.scale), 0.0f) & 0xFFFFu);
                 } else if (P.out_mode == SK_OUT_F32) {
                     float* out = static_cast<float*>(P.out) + (int64_t)m * P.out_ld;
 #pragma unroll

@@ -266,6 +266,106 @@ qlora_status qlora_fused_linear_bwd(const void *dY, const void *X, int64_t M, co
                                     qlora_stream_t stream);
 
 /*
+ * Dropout from a counter-based generator.  The keep mask is never stored:
+ * every kernel that needs it recomputes it from (seed, offset, element index).
+ *   generator  Philox-4x32-10 (Salmon et al., "Parallel random numbers: as
+ *              easy as 1, 2, 3", 2011), key = seed, counter = (block number,
+ *              offset).  A block gives the 15-bit numbers of eight consecutive
+ *              elements: the low 15 bits of the low, then of the high half of
+ *              each of its four words.  Element e (flattened row-major) is
+ *              number e % 8 of block e / 8.
+ *   keep       number >= T, T = round(2^15 p): probability 1 - T / 2^15.
+ *   factor     kept elements are multiplied by 2^15 / (2^15 - T).
+ * A probability below 2^-16 rounds to no dropout; p must be at least 0 and
+ * below 1 - 2^-16 (INVALID_ARG otherwise).  The same (seed, offset) gives the
+ * same mask; give every call of a step that needs its own mask its own offset.
+ *   offset_dev  device pointer to a 64-bit counter, or NULL.  Where it is
+ *              given, the kernels add its value, read when they run, to
+ *              `offset`: a captured graph draws new masks at every replay once
+ *              the program advances the counter between replays.  8-byte
+ *              aligned; not written, and not to be written, by anything that
+ *              runs beside the call.
+ */
+typedef struct {
+    float p;
+    uint64_t seed;
+    uint64_t offset;
+    const uint64_t *offset_dev;
+} qlora_dropout_config;
+
+/*
+ * Y[e] = kept(e) ? X[e] * factor : +0 for n elements of bf16 or fp32 (formed
+ * in fp32, rounded once).  A dropped element gives +0 whatever X holds there,
+ * NaN and infinities too.  The gradient of Y = dropout(X) is the same call on
+ * dY with the same configuration.  Y may be X itself; otherwise they must not
+ * overlap.  X and Y 16-byte aligned, n >= 0; drop must not be NULL.
+ */
+qlora_status qlora_dropout(const void *X, qlora_dtype dtype, int64_t n, const qlora_dropout_config *drop,
+                           void *Y, qlora_stream_t stream);
+
+/*
+ * The fused projection (qlora_fused_linear_fwd / _bwd; nseg == 1: the plain
+ * linear) whose adapters read dropout(X) (`lora_dropout` of LoraConfig,
+ * reproduction blog): with keep [M, K] the mask of X's elements and
+ * s' = scale * factor (rounded to fp32),
+ *   Xd = keep * X,   U = s' Xd A^T,   Y[:, seg i] = X w'_i^T + U_i B_i^T
+ *   G_i = s' dY[:, seg i] B_i,   dX = sum_i dY[:, seg i] w'_i + keep * (G A)
+ *   dA = G^T Xd,   dB_i = dY[:, seg i]^T U_i
+ * One mask serves every adapter of the projection.  Dropped elements of X
+ * count as 0 in the adapter whatever they hold.  drop == NULL, or a
+ * probability that rounds to 0, is no dropout.
+ * grad_dtype: element type of dA and dB, fp32 (for qlora_adamw_step) or bf16
+ * (the adapters' own type).  dX may be NULL.  With M == 0, dA and dB are set
+ * to zero.  Other arguments, requirements, streams and errors as for
+ * qlora_fused_linear_fwd / _bwd; the workspace query is the one below.
+ */
+size_t qlora_fused_linear_dropout_workspace(int64_t M, const qlora_nf4_weight *w, int32_t nseg, int32_t r,
+                                            int32_t bwd);
+qlora_status qlora_fused_linear_dropout_fwd(const void *X, int64_t M, const qlora_nf4_weight *w, int32_t nseg,
+                                            const void *A, const void *B, int32_t r, float scale,
+                                            const qlora_dropout_config *drop, void *Y, void *ws,
+                                            size_t ws_bytes, qlora_stream_t stream);
+qlora_status qlora_fused_linear_dropout_bwd(const void *dY, const void *X, int64_t M,
+                                            const qlora_nf4_weight *w, int32_t nseg, const void *A,
+                                            const void *B, int32_t r, float scale,
+                                            const qlora_dropout_config *drop, void *dX,
+                                            qlora_dtype grad_dtype, void *dA, void *dB, void *ws,
+                                            size_t ws_bytes, qlora_stream_t stream);
+
+/*
+ * Gated feed-forward block over one quantized weight w [2F, K], the gate rows
+ * and then the up rows (the gate/up fused projection above, nseg == 2), each
+ * half with its own rank-r adapter and, with drop, one dropout mask on the
+ * adapters' input:
+ *   [g | u] = the fused projection's Y (kept in fp32),   H = act(g) u
+ *   X [M, K] bf16, H [M, F] bf16 (written), GU [M, 2F] bf16 (written with
+ *   [g | u] rounded once, for the backward; NULL to skip).
+ * act: QLORA_ACT_SILU, g / (1 + exp(-g)), or QLORA_ACT_GELU_TANH,
+ * g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))).
+ * Backward, from dH [M, F] and the kept GU:
+ *   dY = [dH u act'(g) | dH act(g)] (rounded to bf16),
+ *   dX, dA, dB = those of qlora_fused_linear_dropout_bwd for this dY.
+ *   dX may be NULL.  grad_dtype as above.
+ * A [2r, K], B [2F, r].  Requirements of the fused projection: F % 256 == 0,
+ * K % 64 == 0, r % 8 == 0, 2r <= 256.  r == 0: no adapters.  M >= 0 (M == 0
+ * writes dA = dB = 0 only).  An unknown act is INVALID_ARG.  Outputs and
+ * inputs must not overlap.
+ */
+#define QLORA_ACT_SILU 0
+#define QLORA_ACT_GELU_TANH 1
+
+size_t qlora_gated_linear_workspace(int64_t M, const qlora_nf4_weight *w, int32_t r, int32_t bwd);
+qlora_status qlora_gated_linear_fwd(const void *X, int64_t M, const qlora_nf4_weight *w, const void *A,
+                                    const void *B, int32_t r, float scale, int32_t act,
+                                    const qlora_dropout_config *drop, void *H, void *GU, void *ws,
+                                    size_t ws_bytes, qlora_stream_t stream);
+qlora_status qlora_gated_linear_bwd(const void *dH, const void *X, const void *GU, int64_t M,
+                                    const qlora_nf4_weight *w, const void *A, const void *B, int32_t r,
+                                    float scale, int32_t act, const qlora_dropout_config *drop, void *dX,
+                                    qlora_dtype grad_dtype, void *dA, void *dB, void *ws, size_t ws_bytes,
+                                    qlora_stream_t stream);
+
+/*
  * LoRA merge (QLoRA tutorial "11.3 QLoRA", pitfalls: merging the adapter
  * into a 4-bit base adds error, so the base is dequantized first; LoRA
  * reproduction blog, "LoRA formula and tensor shapes": the adapter adds

@@ -307,3 +307,111 @@ def adamw_step(p: np.ndarray, m: np.ndarray, v: np.ndarray, grad: np.ndarray, *,
     g = np.ascontiguousarray(grad, np.float64)
     lib().oracle_adamw_step(p.size, float(lr), float(beta1), float(beta2), float(eps), float(weight_decay),
                             float(grad_scale), int(step), _ptr(p), _ptr(m), _ptr(v), _ptr(g))
+
+
+# --------------------------------------------------------------------------
+# dropout and the gated feed-forward, in fp64 (NumPy)
+# --------------------------------------------------------------------------
+DROP_STEPS = 1 << 15
+
+
+def philox4x32(counter, key, rounds: int = 10):
+    """Philox-4x32 of one counter (4 words) and key (2 words), in Python
+    integers: the published round, two 32 x 32 -> 64 bit products."""
+    c, k = [int(x) for x in counter], [int(x) for x in key]
+    for _ in range(rounds):
+        p0, p1 = c[0] * 0xD2511F53, c[2] * 0xCD9E8D57
+        c = [(p1 >> 32) ^ c[1] ^ k[0], p1 & 0xFFFFFFFF, (p0 >> 32) ^ c[3] ^ k[1], p0 & 0xFFFFFFFF]
+        k = [(k[0] + 0x9E3779B9) & 0xFFFFFFFF, (k[1] + 0xBB67AE85) & 0xFFFFFFFF]
+    return c
+
+
+def dropout_threshold(p: float) -> int:
+    """T = round(2^15 p), halves up."""
+    return int(np.floor(float(np.float32(p)) * DROP_STEPS + 0.5))
+
+
+def dropout_keep(n: int, p: float, seed: int, offset: int = 0, first: int = 0) -> np.ndarray:
+    """Keep mask of the elements first .. first + n - 1 (first a multiple of 8)."""
+    assert first % 8 == 0
+    T = dropout_threshold(p)
+    if T == 0:
+        return np.ones(n, bool)
+    blk = np.arange(first // 8, (first + n + 7) // 8, dtype=np.uint64)
+    lo, s32 = np.uint64(0xFFFFFFFF), np.uint64(32)
+    c = [blk & lo, blk >> s32, np.full_like(blk, offset & 0xFFFFFFFF), np.full_like(blk, (offset >> 32) & 0xFFFFFFFF)]
+    k = [seed & 0xFFFFFFFF, (seed >> 32) & 0xFFFFFFFF]
+    for _ in range(10):
+        p0, p1 = c[0] * np.uint64(0xD2511F53), c[2] * np.uint64(0xCD9E8D57)
+        c = [(p1 >> s32) ^ c[1] ^ np.uint64(k[0]), p1 & lo, (p0 >> s32) ^ c[3] ^ np.uint64(k[1]), p0 & lo]
+        k = [(k[0] + 0x9E3779B9) & 0xFFFFFFFF, (k[1] + 0xBB67AE85) & 0xFFFFFFFF]
+    num = np.stack([h for w in c for h in (w & np.uint64(0x7FFF), (w >> np.uint64(16)) & np.uint64(0x7FFF))], axis=1)
+    return num.reshape(-1)[:n] >= T
+
+
+def dropout_factor(p: float) -> float:
+    return DROP_STEPS / (DROP_STEPS - dropout_threshold(p))
+
+
+def _f64(bits: np.ndarray) -> np.ndarray:
+    """bf16 bits as fp64 values."""
+    return (_bits(bits).astype(np.uint32) << 16).view(np.float32).astype(np.float64)
+
+
+def _drop_mask(shape, drop) -> tuple[np.ndarray, float]:
+    """(mask [M, K], factor) of drop = (p, seed, offset) or None."""
+    if drop is None:
+        return np.ones(shape, bool), 1.0
+    return dropout_keep(int(np.prod(shape)), *drop).reshape(shape), dropout_factor(drop[0])
+
+
+def dropout_linear_fwd(X, W, A, B, s: float, nseg: int, drop) -> np.ndarray:
+    """Fused projection whose adapters read dropout(X): Y in fp64."""
+    x, w, a, b = map(_f64, (X, W, A, B))
+    mask, up = _drop_mask(x.shape, drop)
+    S, r = w.shape[0] // nseg, a.shape[0] // nseg
+    u = s * up * (np.where(mask, x, 0.0) @ a.T)
+    lora = [u[:, i * r:(i + 1) * r] @ b[i * S:(i + 1) * S].T for i in range(nseg)]
+    return x @ w.T + np.concatenate(lora, axis=1)
+
+
+def dropout_linear_bwd(dY: np.ndarray, X, W, A, B, s: float, nseg: int, drop):
+    """(dX, dA, dB) in fp64; dY is fp64 values."""
+    x, w, a, b = map(_f64, (X, W, A, B))
+    mask, up = _drop_mask(x.shape, drop)
+    S, r = w.shape[0] // nseg, a.shape[0] // nseg
+    xd = np.where(mask, x, 0.0)
+    u = s * up * (xd @ a.T)
+    g = s * up * np.concatenate([dY[:, i * S:(i + 1) * S] @ b[i * S:(i + 1) * S] for i in range(nseg)], axis=1)
+    dB = np.concatenate([dY[:, i * S:(i + 1) * S].T @ u[:, i * r:(i + 1) * r] for i in range(nseg)], axis=0)
+    return dY @ w + np.where(mask, g @ a, 0.0), g.T @ xd, dB
+
+
+def gated_act(act: str, g: np.ndarray) -> tuple[np.ndarray, np.ndarray]:
+    """(act(g), act'(g)) in fp64."""
+    if act == "silu":
+        sig = 1.0 / (1.0 + np.exp(-g))
+        return g * sig, sig + g * sig * (1.0 - sig)
+    c = np.sqrt(2.0 / np.pi)
+    t = np.tanh(c * (g + 0.044715 * g ** 3))
+    return 0.5 * g * (1.0 + t), 0.5 * (1.0 + t) + 0.5 * g * (1.0 - t * t) * c * (1.0 + 3 * 0.044715 * g * g)
+
+
+def gated_fwd(X, W, A, B, s: float, act: str, drop):
+    """(H, GU) in fp64 of the gated feed-forward block."""
+    y = dropout_linear_fwd(X, W, A, B, s, 2, drop)
+    F = y.shape[1] // 2
+    return gated_act(act, y[:, :F])[0] * y[:, F:], y
+
+
+def gated_grad(dH, GU, act: str) -> np.ndarray:
+    """[dH u act'(g) | dH act(g)] in fp64 from bf16 bits."""
+    dh, gu = _f64(dH), _f64(GU)
+    F = dh.shape[1]
+    v, d = gated_act(act, gu[:, :F])
+    return np.concatenate([dh * gu[:, F:] * d, dh * v], axis=1)
+
+
+def gated_bwd(dH, X, GU, W, A, B, s: float, act: str, drop):
+    """(dX, dA, dB) in fp64 of the gated feed-forward block."""
+    return dropout_linear_bwd(gated_grad(dH, GU, act), X, W, A, B, s, 2, drop)

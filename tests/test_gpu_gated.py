@@ -1,0 +1,282 @@
+"""GPU gated feed-forward block against fp64: H and the kept pre-activations
+for every token count class, both activations, with and without adapters and
+dropout; the backward from the kept values; a whole training step.
+
+Tolerances: H and GU carry their own bf16 rounding and, in the adapter's term,
+that of U; the backward's dY is rounded once to bf16 and reaches dX, G and dB,
+which add their own and G's or U's rounding: at most three roundings of 1.7e-3
+of the norm each, sqrt(3) * 1.7e-3 = 2.9e-3, below the linear tests' 5e-3.
+The largest error of a sum of many rounded terms stays below 1e-2 of the
+largest value.  For few tokens the weight's values carry up to 1.6e-3 of bf16
+table error, which the activation and the product pass on at most about
+threefold (g act'(g) / act(g) <= 1 + |g| / 2 at the values met, u once)."""
+import numpy as np
+import pytest
+import torch
+
+from bit_nf4_quantized_08_b200 import workloads as wl
+from conftest import assert_close_tol
+from test_gpu_canary import Guarded
+
+pytestmark = pytest.mark.gpu
+
+
+def _same_bits(a, b):
+    it = torch.int16 if a.dtype == torch.bfloat16 else torch.int32
+    return torch.equal(a.contiguous().view(it), b.contiguous().view(it))
+
+
+def _setup(Q, M, F, K, r, seed, dq=True, w_std=None, **fmt):
+    # pre-activations of about N(0, 1), as a trained block's
+    W = wl.weight(2 * F, K, seed=seed, dtype=torch.bfloat16)
+    W = (W.float() * ((w_std or K ** -0.5) / 0.02)).to(torch.bfloat16)
+    inp = wl.fused_inputs(M, 2, F, K, max(r, 8), seed=seed, b_std=0.3)
+    inp["dH"] = inp.pop("dY")[:, :F].contiguous()
+    if r == 0:
+        inp["A"] = inp["B"] = None
+    q = Q.qlora_nf4_quantize(W.cuda(), double_quant=dq, **fmt)
+    return q, inp, wl.bits(Q.qlora_nf4_dequantize(q).cpu())
+
+
+def _dev(inp):
+    return {k: None if v is None else v.cuda() for k, v in inp.items()}
+
+
+def _bits_or_zero(t, shape):
+    return np.zeros(shape, np.uint16) if t is None else wl.bits(t)
+
+
+def _np(t):
+    return t.double().cpu().numpy()
+
+
+def _check(Q, O, q, inp, Wd, s, act, drop, tag, grad_dtype=torch.float32, want_dx=True):
+    t = _dev(inp)
+    H, GU = Q.qlora_gated_linear_fwd(t["X"], q, t["A"], t["B"], s, act, drop, want_gu=True)
+    H2, none = Q.qlora_gated_linear_fwd(t["X"], q, t["A"], t["B"], s, act, drop)
+    g = Q.qlora_gated_linear_bwd(t["dH"], t["X"], GU, q, t["A"], t["B"], s, act, drop, want_dx=want_dx,
+                                 grad_dtype=grad_dtype)
+    torch.cuda.synchronize()
+    assert Q.qlora_get_last_error() == 0
+    assert none is None and _same_bits(H, H2), f"{tag}: H depends on whether GU is kept"
+    N, K = Wd.shape
+    bits = (wl.bits(inp["X"]), Wd, _bits_or_zero(inp["A"], (16, K)), _bits_or_zero(inp["B"], (N, 8)))
+    d = None if drop is None else (drop.p, drop.seed, drop.offset)
+    rH, rGU = O.gated_fwd(*bits, s, act, d)
+    assert_close_tol(_np(H), rH, f"H {tag}")
+    assert_close_tol(_np(GU), rGU, f"GU {tag}")
+    # the backward is a function of the kept (rounded) GU
+    ref = O.gated_bwd(wl.bits(inp["dH"]), bits[0], wl.bits(GU.cpu()), *bits[1:], s, act, d)
+    for name, got, r in zip(("dX", "dA", "dB"), g, ref):
+        if got is not None:
+            assert_close_tol(_np(got), r, f"{name} {tag}")
+    return H, GU, g
+
+
+CASES = [
+    # M, F, K, r: one token, every small-token kernel and its borders, ragged token tiles, several column tiles
+    (1, 256, 64, 8), (2, 512, 128, 16), (15, 256, 320, 64), (16, 768, 448, 24), (17, 256, 192, 8), (31, 512, 256, 40),
+    (33, 256, 512, 128), (64, 1024, 256, 64), (65, 256, 64, 8), (129, 512, 320, 16), (300, 256, 512, 32),
+    (513, 768, 576, 64), (1100, 512, 192, 128),
+]
+
+
+@pytest.mark.parametrize("M,F,K,r", CASES)
+@pytest.mark.parametrize("act,p", [("silu", 0.3), ("gelu_tanh", 0.0)])
+def test_gated_parity(Q, O, cuda, M, F, K, r, act, p):
+    q, inp, Wd = _setup(Q, M, F, K, r, seed=100 + M)
+    drop = Q.Dropout(p, 31, 2) if p else None
+    _check(Q, O, q, inp, Wd, 2.0, act, drop, f"M={M} F={F} K={K} r={r} {act}",
+           torch.bfloat16 if M % 2 else torch.float32)
+
+
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_gated_without_adapter(Q, O, cuda, M):
+    q, inp, Wd = _setup(Q, M, 512, 320, 0, seed=7)
+    _, _, g = _check(Q, O, q, inp, Wd, 1.0, "silu", None, f"r=0 M={M}")
+    assert g[1] is None and g[2] is None
+    # a dropout without an adapter drops nothing
+    t = _dev(inp)
+    H, _ = Q.qlora_gated_linear_fwd(t["X"], q, None, None, 1.0, "silu", Q.Dropout(0.5, 1))
+    assert _same_bits(H, Q.qlora_gated_linear_fwd(t["X"], q, None, None, 1.0, "silu")[0])
+
+
+@pytest.mark.parametrize("fmt", [dict(dq=False), dict(blocksize=128, code_type="fp4"), dict(blocksize=256, dq_type="e4m3")],
+                         ids=["no_dq", "fp4_128", "e4m3_256"])
+@pytest.mark.parametrize("M", [6, 50, 200])
+def test_gated_formats(Q, O, cuda, fmt, M):
+    q, inp, Wd = _setup(Q, M, 512, 512, 16, seed=8, **fmt)
+    _check(Q, O, q, inp, Wd, 2.0, "silu", Q.Dropout(0.1, 1, 1), f"{fmt} M={M}")
+
+
+@pytest.mark.parametrize("mode", [2, 3, 4, 6, 7, 8], ids=["streamk7", "single_cta_grid", "pair_streamk4", "serial_bwd",
+                                                          "warp_mma", "tcgen05_small"])
+@pytest.mark.parametrize("M", [10, 30, 600])
+def test_gated_alternate_schedules(Q, O, cuda, mode, M):
+    q, inp, Wd = _setup(Q, M, 512, 512, 16, seed=9)
+    Q.qlora_debug_inject(mode)
+    try:
+        _check(Q, O, q, inp, Wd, 2.0, "silu", Q.Dropout(0.1, 4, 4), f"mode {mode} M={M}")
+    finally:
+        Q.qlora_debug_inject(0)
+
+
+@pytest.mark.parametrize("M", [4, 20, 200])
+def test_gated_saturated_activations(Q, O, cuda, M):
+    """Pre-activations of a few hundred: exp overflows and vanishes, H and the gradients stay finite and right."""
+    for act in ("silu", "gelu_tanh"):
+        q, inp, Wd = _setup(Q, M, 256, 256, 8, seed=10, w_std=10.0)
+        with np.errstate(over="ignore"):
+            _check(Q, O, q, inp, Wd, 1.0, act, None, f"saturated {act} M={M}")
+
+
+@pytest.mark.parametrize("M", [3, 24, 70, 333])
+def test_gated_guards_and_repeat(Q, cuda, M):
+    F, K, r = 512, 320, 24
+    q, inp, _ = _setup(Q, M, F, K, r, seed=11)
+    t = _dev(inp)
+    drop = Q.Dropout(0.15, 2, 2)
+    outs = []
+    for _ in range(2):
+        G = {"H": Guarded((M, F), torch.bfloat16), "GU": Guarded((M, 2 * F), torch.bfloat16),
+             "dX": Guarded((M, K), torch.bfloat16), "dA": Guarded((2 * r, K), torch.float32),
+             "dB": Guarded((2 * F, r), torch.float32),
+             "wf": Guarded((Q.qlora_gated_linear_workspace(M, q, r, False),), torch.uint8),
+             "wb": Guarded((Q.qlora_gated_linear_workspace(M, q, r, True),), torch.uint8)}
+        Q.qlora_gated_linear_fwd(t["X"], q, t["A"], t["B"], 2.0, "silu", drop, H=G["H"].t, GU=G["GU"].t, ws=G["wf"].t)
+        Q.qlora_gated_linear_bwd(t["dH"], t["X"], G["GU"].t, q, t["A"], t["B"], 2.0, "silu", drop, dX=G["dX"].t,
+                                 dA=G["dA"].t, dB=G["dB"].t, ws=G["wb"].t)
+        torch.cuda.synchronize()
+        assert Q.qlora_get_last_error() == 0
+        for k, g in G.items():
+            g.check(k)
+        outs.append([G[k].t.clone() for k in ("H", "GU", "dX", "dA", "dB")])
+    assert all(_same_bits(a, b) for a, b in zip(*outs))
+
+
+def test_gated_empty_batch_and_refusals(Q, cuda):
+    q, inp, _ = _setup(Q, 4, 256, 128, 8, seed=12)
+    t = _dev(inp)
+    X = torch.empty(0, 128, dtype=torch.bfloat16, device=cuda)
+    H, GU = Q.qlora_gated_linear_fwd(X, q, t["A"], t["B"], 1.0, want_gu=True)
+    assert H.shape == (0, 256) and GU.shape == (0, 512)
+    dA = torch.ones(16, 128, device=cuda)
+    dX, dA, dB = Q.qlora_gated_linear_bwd(H, X, GU, q, t["A"], t["B"], 1.0, dA=dA)
+    torch.cuda.synchronize()
+    assert not dA.any() and not dB.any()
+    with pytest.raises(ValueError):
+        Q.qlora_gated_linear_fwd(t["X"], q, t["A"], t["B"], 1.0, act="relu")
+    with pytest.raises(ValueError):
+        Q.qlora_gated_linear_fwd(t["X"][:, ::2], q, t["A"], t["B"], 1.0)
+    with pytest.raises(Q.QloraError) as e:
+        Q.qlora_gated_linear_fwd(t["X"], q, t["A"], t["B"], 1.0, dropout=Q.Dropout(1.0, 1))
+    assert e.value.status == Q.QLORA_ERR_INVALID_ARG
+
+
+def test_gated_graph_and_shared_workspace(Q, cuda):
+    """Two captured graphs that share one workspace, replayed in turn, and eager calls between."""
+    sets = []
+    for i, M in enumerate((5, 300)):
+        q, inp, _ = _setup(Q, M, 512, 256, 16, seed=13 + i)
+        sets.append((q, _dev(inp), Q.Dropout(0.2, i, 1)))
+    need = max(Q.qlora_gated_linear_workspace(t["X"].shape[0], q, 16, b) for q, t, _ in sets for b in (False, True))
+    ws = torch.empty(need, dtype=torch.uint8, device=cuda)
+
+    def step(q, t, d):
+        H, GU = Q.qlora_gated_linear_fwd(t["X"], q, t["A"], t["B"], 2.0, "silu", d, want_gu=True, ws=ws)
+        return (H, GU, *Q.qlora_gated_linear_bwd(t["dH"], t["X"], GU, q, t["A"], t["B"], 2.0, "silu", d, ws=ws))
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graphs, outs = [], []
+    with torch.cuda.stream(s):
+        ref = [[x.clone() for x in step(*a)] for a in sets]
+        for a in sets:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=s):
+                outs.append(step(*a))
+            graphs.append(g)
+        for i in (0, 1, 1, 0, 1):
+            for o in outs[i]:
+                o.fill_(0)
+            graphs[i].replay()
+            step(*sets[1 - i])
+            s.synchronize()
+            assert all(_same_bits(a, b) for a, b in zip(outs[i], ref[i])), i
+    assert Q.qlora_get_last_error() == 0
+
+
+@pytest.mark.parametrize("M,F,K", [(1, 11008, 4096), (16, 11008, 4096), (48, 11008, 4096), (2048, 11008, 4096),
+                                   (777, 22016, 8192)])
+def test_gated_full_size(Q, O, cuda, M, F, K):
+    """LLaMA-7B (all token classes) and LLaMA-65B gate/up, fp64 on the device."""
+    r, s, p = 64, 0.25, 0.05
+    q, inp, _ = _setup(Q, M, F, K, r, seed=14, w_std=0.02)
+    t = _dev(inp)
+    drop = Q.Dropout(p, 5, 5)
+    H, GU = Q.qlora_gated_linear_fwd(t["X"], q, t["A"], t["B"], s, "silu", drop, want_gu=True)
+    dX, dA, dB = Q.qlora_gated_linear_bwd(t["dH"], t["X"], GU, q, t["A"], t["B"], s, "silu", drop)
+    torch.cuda.synchronize()
+    assert Q.qlora_get_last_error() == 0
+    mask = torch.from_numpy(O.dropout_keep(M * K, p, 5, 5).reshape(M, K)).cuda().double()
+    W = Q.qlora_nf4_dequantize(q).double()
+    X, A, B, dH = (t[k].double() for k in ("X", "A", "B", "dH"))
+    s1 = s * O.dropout_factor(p)
+    xd = X * mask
+    u = s1 * xd @ A.T
+    Y = X @ W.T
+    Y[:, :F] += u[:, :r] @ B[:F].T
+    Y[:, F:] += u[:, r:] @ B[F:].T
+    assert_close_tol(_np(GU), Y.cpu().numpy(), "GU")
+    sig = torch.sigmoid(Y[:, :F])
+    assert_close_tol(_np(H), (Y[:, :F] * sig * Y[:, F:]).cpu().numpy(), "H")
+    g, up = GU[:, :F].double(), GU[:, F:].double()
+    sig = torch.sigmoid(g)
+    dY = torch.cat([dH * up * sig * (1 + g * (1 - sig)), dH * g * sig], dim=1)
+    G = s1 * torch.cat([dY[:, :F] @ B[:F], dY[:, F:] @ B[F:]], dim=1)
+    assert_close_tol(_np(dX), (dY @ W + (G @ A) * mask).cpu().numpy(), "dX")
+    assert_close_tol(_np(dA), (G.T @ xd).cpu().numpy(), "dA")
+    assert_close_tol(_np(dB), torch.cat([dY[:, :F].T @ u[:, :r], dY[:, F:].T @ u[:, r:]]).cpu().numpy(), "dB")
+
+
+def test_feed_forward_training_step(Q, O, cuda):
+    """The operators as a step uses them: gate/up with dropout, the down projection with its own, residual dropout,
+    the backward of all three, and the adapters' optimizer step; each against fp64 on what the one before gave."""
+    M, F, K, r, s = 260, 512, 256, 16, 2.0
+    q1, inp, W1 = _setup(Q, M, F, K, r, seed=15)
+    t = _dev(inp)
+    Wdn = wl.weight(K, F, seed=16, dtype=torch.bfloat16)
+    q2 = Q.qlora_nf4_quantize(Wdn.cuda())
+    W2 = wl.bits(Q.qlora_nf4_dequantize(q2).cpu())
+    i2 = wl.linear_inputs(M, K, F, r, seed=17)
+    A2, B2, dO = i2["A"].cuda(), (i2["B"].float() * 30).to(torch.bfloat16).cuda(), i2["dY"].cuda()
+    d1, d2, d3 = Q.Dropout(0.1, 40, 0), Q.Dropout(0.1, 40, 1), Q.Dropout(0.2, 40, 2)
+    H, GU = Q.qlora_gated_linear_fwd(t["X"], q1, t["A"], t["B"], s, "silu", d1, want_gu=True)
+    Yd = Q.qlora_fused_linear_dropout_fwd(H, q2, 1, A2, B2, s, d2)
+    out = Q.qlora_dropout(Yd, d3)
+    dYd = Q.qlora_dropout(dO, d3)
+    dH, dA2, dB2 = Q.qlora_fused_linear_dropout_bwd(dYd, H, q2, 1, A2, B2, s, d2)
+    dX, dA1, dB1 = Q.qlora_gated_linear_bwd(dH, t["X"], GU, q1, t["A"], t["B"], s, "silu", d1)
+    flat_g = torch.cat([x.reshape(-1) for x in (dA1, dB1, dA2, dB2)])
+    p = torch.cat([x.float().reshape(-1) for x in (t["A"], t["B"], A2, B2)])
+    m, v, pb, p0 = torch.zeros_like(p), torch.zeros_like(p), torch.empty_like(p, dtype=torch.bfloat16), p.cpu().double().numpy()
+    Q.qlora_adamw_step(p, m, v, flat_g, pb, lr=1e-3, step=1)
+    torch.cuda.synchronize()
+    assert Q.qlora_get_last_error() == 0
+    b = lambda x: wl.bits(x.cpu())
+    rH, _ = O.gated_fwd(b(t["X"]), W1, b(t["A"]), b(t["B"]), s, "silu", (0.1, 40, 0))
+    assert_close_tol(_np(H), rH, "H")
+    assert_close_tol(_np(Yd), O.dropout_linear_fwd(b(H), W2, b(A2), b(B2), s, 1, (0.1, 40, 1)), "down")
+    keep = O.dropout_keep(M * K, 0.2, 40, 2).reshape(M, K)
+    assert np.array_equal(_np(out) != 0, keep & (_np(Yd) != 0))
+    assert np.array_equal(_np(dYd) != 0, keep & (_np(dO) != 0))
+    for got, ref in zip((dH, dA2, dB2), O.dropout_linear_bwd(_np(dYd), b(H), W2, b(A2), b(B2), s, 1, (0.1, 40, 1))):
+        assert_close_tol(_np(got), ref, "down backward")
+    for got, ref in zip((dX, dA1, dB1), O.gated_bwd(b(dH), b(t["X"]), b(GU), W1, b(t["A"]), b(t["B"]), s, "silu",
+                                                    (0.1, 40, 0))):
+        assert_close_tol(_np(got), ref, "gate/up backward")
+    # the first AdamW step moves every parameter against its gradient by lr (up to eps)
+    g = flat_g.cpu().double().numpy()
+    big = np.abs(g) > 1e-4
+    step = _np(p) - p0
+    assert np.max(np.abs(step[big] + 1e-3 * np.sign(g[big]))) <= 1e-3 * 1e-3 + 2.0 ** -23 * np.max(np.abs(p0))
