@@ -64,6 +64,10 @@ struct GemmParams {
     // segment, starting at (n0 / lora_seg_rows) * lora_seg_r; 0 = one adapter
     int lora_seg_rows, lora_seg_r;
     int code_type;  // 4-bit code book of the weight (0 NF4, 1 FP4)
+    // gated form of the pair kernel (out = H [M][F]): F, the activation, and
+    // the map of the kept pre-activations [M][2F] where keep_gu
+    int gate_rows, act, keep_gu;
+    CUtensorMap tmGU;
 };
 
 // First sU column of the adapter of the output rows starting at n0.

@@ -18,6 +18,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "gated.cuh"
 #include "gemm.cuh"
 #include "nf4.cuh"
 
@@ -100,9 +101,21 @@ struct PairSchedule {
     __device__ bool more() const { return SK && pos < end; }
 };
 
-template <int DQ, int STAGES, bool SK>
+// GATED (the gated feed-forward's forward, H = act(g) u): an output tile is
+// 512 tokens x 128 columns of H.  The leader's half of Bop is 128 gate rows of
+// the weight and its peer's the matching 128 up rows, so that after the main
+// loop every accumulator row of either CTA holds g in columns 0..127 and u in
+// columns 128..255 of the same 128 hidden columns: the activation and the
+// product are formed from the fp32 accumulators of one thread, and neither g
+// nor u goes through memory (they are also stored, rounded, where the caller
+// keeps them for the backward).  The two adapters share ceil(2r / 64) LoRA
+// k-steps over sU = [U_gate | U_up]: the leader's B tile starts at column 0 of
+// its adapter and its peer's at column -r, and the loads' zero fill to the
+// left and right makes the block-diagonal operand.
+template <int DQ, int STAGES, bool SK, bool GATED = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREADS, 1)
     k_gemm_pair(const __grid_constant__ GemmParams p) {
+    static_assert(!GATED || (DQ == DQ_B_K && !SK), "the gated form is a forward on the grid schedule");
     using S = PairShape<DQ>;
     constexpr int B_MN = DQ == DQ_B_MN ? 1 : 0;
     extern __shared__ uint8_t smem_raw[];
@@ -146,6 +159,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREA
         prefetch_tensormap(&p.tmA);
         prefetch_tensormap(&p.tmCodes);
         prefetch_tensormap(&p.tmOut);
+        if (GATED && p.keep_gu) prefetch_tensormap(&p.tmGU);
         if (p.ks_lora) {
             prefetch_tensormap(&p.tmA2);
             prefetch_tensormap(&p.tmB2);
@@ -172,7 +186,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREA
             bool ok = true;
             while (ok && sch.next(p, sg)) {
                 const int m0 = sg.tm * 512;
-                const int nb0 = sg.tn * 256 + 128 * (int)rank;  // first Bop column of this CTA
+                // first Bop column (weight row) of this CTA
+                const int nb0 = GATED ? sg.tn * 128 + (int)rank * p.gate_rows : sg.tn * 256 + 128 * (int)rank;
                 for (int k = sg.k0; k < sg.k1; ++k, ++it) {
                     const int s = it % STAGES, u = it / STAGES;
                     if (k >= p.ks_main && !waited) {
@@ -202,14 +217,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREA
                     const CUtensorMap* mA = lora ? &p.tmA2 : &p.tmA;
 #pragma unroll
                     for (int mt = 0; mt < 2; ++mt)
-                        tma_load_2d(sA + mt * 16384, mA, full_tma(s), kc * 64 + (lora ? lora_col0(p, sg.tn * 256) : 0),
+                        tma_load_2d(sA + mt * 16384, mA, full_tma(s),
+                                    kc * 64 + (lora && !GATED ? lora_col0(p, sg.tn * 256) : 0),
                                     m0 + 256 * mt + 128 * (int)rank);
                     if (lora) {
                         if (B_MN) {
                             for (int c = 0; c < 2; ++c)
                                 tma_load_2d(sB + 8192 * c, &p.tmB2, full_tma(s), nb0 + 64 * c, kc * 64);
                         } else {
-                            tma_load_2d(sB, &p.tmB2, full_tma(s), kc * 64, nb0);
+                            tma_load_2d(sB, &p.tmB2, full_tma(s),
+                                        kc * 64 - (GATED && rank ? p.lora_seg_r : 0), nb0);
                         }
                     } else if (DQ == DQ_B_K) {
                         tma_load_2d(sC, &p.tmCodes, full_tma(s), kc * 32, nb0);
@@ -416,7 +433,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREA
                     bulk_load(pf_base + 16384u * j, chunk_src(j), 16384, pf_full(j));
                 }
             }
-            if (!skip) {
+            if (GATED && !skip) {
+                // panels of 128 rows x 64 columns: H 0..3, then g 4 + 4 mt + 0..1 and u 4 + 4 mt + 2..3
+                static_assert(12 * 16384 <= S::STAGE_BYTES * STAGES, "the gated epilogue's panels fit the stage buffers");
+                const int act = p.act;
+                const bool keep = p.keep_gu != 0;
+#pragma unroll 1
+                for (int itc = 0; itc < 8; ++itc) {
+                    const int mt = itc >> 2, col0 = (itc & 3) * 32;
+                    uint32_t g[32], u[32];
+                    __syncwarp();
+                    const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(mt * 256 + col0);
+                    tmem_ld_32x32b_x32(ta, g);
+                    tmem_ld_32x32b_x32(ta + 128u, u);
+                    tmem_ld_wait();
+                    const uint32_t hp = base + (uint32_t)(mt * 2 + (col0 >> 6)) * 16384u;
+                    const uint32_t gp = base + (uint32_t)(4 + mt * 4 + (col0 >> 6)) * 16384u;
+                    const uint32_t row0 = (uint32_t)row * 128u + (uint32_t)((col0 & 63) >> 3) * 16u;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t h[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int e = 8 * q + 2 * i;
+                            h[i] = pack_bf16x2(act_value(act, __uint_as_float(g[e])) * __uint_as_float(u[e]),
+                                               act_value(act, __uint_as_float(g[e + 1])) * __uint_as_float(u[e + 1]));
+                        }
+                        st_shared_v4(hp + sw128(row0 + 16u * q), h[0], h[1], h[2], h[3]);
+                    }
+                    if (keep) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int e = 8 * q + 2 * i;
+                                w[i] = pack_bf16x2(__uint_as_float(g[e]), __uint_as_float(g[e + 1]));
+                                w[4 + i] = pack_bf16x2(__uint_as_float(u[e]), __uint_as_float(u[e + 1]));
+                            }
+                            st_shared_v4(gp + sw128(row0 + 16u * q), w[0], w[1], w[2], w[3]);
+                            st_shared_v4(gp + 2u * 16384u + sw128(row0 + 16u * q), w[4], w[5], w[6], w[7]);
+                        }
+                    }
+                }
+            }
+            if (!GATED && !skip) {
 #pragma unroll 1
                 for (int itc = 0; itc < 16; ++itc) {
                     const int mt = itc >> 3, col0 = (itc & 7) * 32;
@@ -492,7 +553,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREA
             if (staged) {
                 fence_proxy_async_smem();
                 named_bar(1, S::NDQ_WARPS * 32);
-                if (ew == 0 && lane == 0 && !skip) {
+                if (GATED && ew == 0 && lane == 0 && !skip) {
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const int y = m0 + 256 * mt + 128 * (int)rank, x = sg.tn * 128 + 64 * c;
+                            tma_store_2d(&p.tmOut, base + (uint32_t)(mt * 2 + c) * 16384u, x, y);
+                            if (p.keep_gu) {
+                                tma_store_2d(&p.tmGU, base + (uint32_t)(4 + mt * 4 + c) * 16384u, x, y);
+                                tma_store_2d(&p.tmGU, base + (uint32_t)(6 + mt * 4 + c) * 16384u, p.gate_rows + x, y);
+                            }
+                        }
+                    bulk_commit_group();
+                    bulk_wait_group_read0();
+                }
+                if (!GATED && ew == 0 && lane == 0 && !skip) {
 #pragma unroll
                     for (int mt = 0; mt < 2; ++mt)
 #pragma unroll

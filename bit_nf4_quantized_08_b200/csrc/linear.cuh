@@ -339,11 +339,13 @@ inline size_t linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int r, int
 // Tile schedule of the dequant GEMMs: stream-K over a persistent grid of
 // one CTA per SM when there are at least two k-steps per CTA, else one CTA
 // per tile.  Debug mode 2 forces stream-K on 7 CTAs (tests of the merge).
-template <int DQ, int STAGES>
+template <int DQ, int STAGES, bool GATED = false>
 inline cudaError_t launch_gemm_pair(const GemmParams& p, dim3 grid, cudaStream_t s, int prof_kind) {
     constexpr int smem = pair_smem_bytes<DQ, STAGES>();
     static_assert(smem <= 232448, "shared memory per CTA");
-    auto kern = p.streamk ? k_gemm_pair<DQ, STAGES, true> : k_gemm_pair<DQ, STAGES, false>;
+    auto kern = GATED       ? k_gemm_pair<DQ, STAGES, false, GATED>
+                : p.streamk ? k_gemm_pair<DQ, STAGES, true>
+                            : k_gemm_pair<DQ, STAGES, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     ProfileScope ps(prof_kind, s);
@@ -402,6 +404,18 @@ inline int pair_active_clusters() {
     return n;
 }
 
+// Grid schedule of the pair GEMM: one pair per tile.
+inline dim3 grid_pair(GemmParams& p, int tiles_n, int tiles_m) {
+    p.tiles_n = tiles_n;
+    p.tiles_total = (int)((int64_t)tiles_n * tiles_m);
+    p.streamk = 0;
+    // token tiles fastest (blockIdx.x / 2), weight column tiles in y (the
+    // grid's y extent is at most 65535: beyond it, columns in x)
+    p.n_in_x = tiles_n > 65535 ? 1 : 0;
+    if (p.n_in_x) return dim3((unsigned)(2 * tiles_n), (unsigned)tiles_m, 1);
+    return dim3((unsigned)(2 * tiles_m), (unsigned)tiles_n, 1);
+}
+
 // Tile schedule of the pair GEMM over tiles_m x tiles_n tiles of 512 x 256:
 // one pair per tile, or (SCHED_PAIR_SK) stream-K over all resident pairs;
 // test mode 4 runs stream-K on 4 pairs, so that tiles are cut between pairs
@@ -423,11 +437,7 @@ inline dim3 schedule_pair(GemmParams& p, int tiles_n, int tiles_m, const LinearW
         p.streamk = 1;
         return dim3((unsigned)(2 * G), 1, 1);
     }
-    // token tiles fastest (blockIdx.x / 2), weight column tiles in y (the
-    // grid's y extent is at most 65535: beyond it, columns in x)
-    p.n_in_x = tiles_n > 65535 ? 1 : 0;
-    if (p.n_in_x) return dim3((unsigned)(2 * tiles_n), (unsigned)tiles_m, 1);
-    return dim3((unsigned)(2 * tiles_m), (unsigned)tiles_n, 1);
+    return grid_pair(p, tiles_n, tiles_m);
 }
 
 inline dim3 schedule_gemm(GemmParams& p, int tiles_n, int tiles_m, const LinearWs& L) {
@@ -687,6 +697,55 @@ inline qlora_status linear_fwd_impl(const void* X, const LinearArgs& a, const vo
     return launch_small_m(X, a, B, Y, L, s);
 }
 
+// H = act(g) u for M > 64 on the gated form of the pair kernel, one pair per
+// tile of 512 tokens x 128 hidden columns whatever schedule the linears use.
+inline qlora_status gated_fwd_large(const void* X, const LinearArgs& a, const void* A, const void* B, int act, void* H,
+                                    void* GU, void* ws, cudaStream_t s) {
+    const qlora_nf4_weight& w = *a.w;
+    const LinearWs L = carve_linear_ws(ws, a.M, a.N, a.K, a.rt(), 0);
+    if (launch_expand_scales(w, L.scales, L.scales_ld, s, nullptr, 0) != cudaSuccess) return QLORA_ERR_CUDA;
+    GemmParams p;
+    memset(&p, 0, sizeof(p));
+    if (!map_bf16(&p.tmA, X, a.K, a.M, 128)) return QLORA_ERR_CUDA;
+    p.tmB = p.tmA2 = p.tmB2 = p.tmA;
+    if (a.r > 0) {
+        SkinnyDesc d;
+        if (!desc_sU(&d, X, a, A, L.sU)) return QLORA_ERR_CUDA;
+        // beside the GEMM, as in linear_fwd_impl
+        const qlora_status st = skinny(&d, 1, a.rt(), s, 1, SKP_PACKED);
+        if (st != QLORA_OK) return st;
+        if (!map_bf16(&p.tmA2, L.sU, a.rt(), a.M, 128)) return QLORA_ERR_CUDA;
+        if (!map_bf16(&p.tmB2, B, a.r, a.N, 128)) return QLORA_ERR_CUDA;
+        p.ks_lora = ceil_div(a.rt(), 64);
+        p.lora_seg_r = a.r;
+        p.late_wait = 1;
+    }
+    if (!map_codes(&p.tmCodes, w, 32, 128)) return QLORA_ERR_CUDA;
+    const int64_t F = a.seg_rows;
+    if (!map_bf16(&p.tmOut, H, F, a.M, 128)) return QLORA_ERR_CUDA;
+    p.tmGU = p.tmOut;
+    if (GU && !map_bf16(&p.tmGU, GU, a.N, a.M, 128)) return QLORA_ERR_CUDA;
+    p.keep_gu = GU ? 1 : 0;
+    p.act = act;
+    p.gate_rows = (int)F;
+    p.scales = L.scales;
+    p.scales_ld = L.scales_ld;
+    p.code_type = w.code_type;
+    p.dq_rows = (int)a.N;
+    p.dq_kbs = (int)(a.K / 64);
+    p.ks_main = (int)(a.K / 64);
+    p.ks_per_split = p.ks_main;
+    p.rows = (int)a.M;
+    p.cols = (int)F;
+    p.out = H;
+    p.out_ld = F;
+    p.timeout_ns = wait_timeout_ns();
+    p.inject = inject_mode() == 1 ? 1 : 0;
+    const dim3 grid = grid_pair(p, ceil_div(F, 128), ceil_div(a.M, 512));
+    return launch_gemm_pair<DQ_B_K, 4, true>(p, grid, s, QLORA_KERNEL_FWD_GEMM) == cudaSuccess ? QLORA_OK
+                                                                                             : QLORA_ERR_CUDA;
+}
+
 // sG = bf16(scale dY B): Aop = dY [m][n] (K-major), Bop = B viewed [j][n] (MN-major).
 // (fused projection: sG = [dY_0 B_0 | dY_1 B_1 | ...], each k-step of dY rows
 // shifted onto its own segment's output columns)
@@ -928,7 +987,7 @@ inline BlockWs carve_block_ws(void* ws, int64_t M, int64_t N, int64_t K, int rt,
     WsCarve c{static_cast<char*>(ws), 0};
     b.linear = c.take(b.linear_bytes);
     b.Xd = rt > 0 ? c.take((size_t)M * K * 2) : nullptr;
-    b.gu = gated ? static_cast<uint16_t*>(c.take((size_t)M * N * 2)) : nullptr;
+    b.gu = gated && (bwd || M <= kSmallM) ? static_cast<uint16_t*>(c.take((size_t)M * N * 2)) : nullptr;
     b.bytes = c.used;
     return b;
 }
@@ -967,6 +1026,7 @@ inline qlora_status gated_fwd_impl(const void* X, LinearArgs a, const void* A, c
     const BlockWs b = carve_block_ws(ws, a.M, a.N, a.K, a.rt(), 0, 1);
     qlora_status st = mask_input(X, a, b, s);
     if (st != QLORA_OK) return st;
+    if (a.M > kSmallM) return gated_fwd_large(X, a, A, B, act, H, GU, b.linear, s);
     uint16_t* gu = GU ? static_cast<uint16_t*>(GU) : b.gu;
     st = linear_fwd_impl(X, a, A, B, gu, b.linear, b.linear_bytes, s);
     if (st != QLORA_OK) return st;
