@@ -74,6 +74,20 @@ __device__ __forceinline__ void drop_mask8(const DropParams& d, uint2 off, uint6
         m[j] = prmt((w[j] & 0x7FFF7FFFu) + d.add, 0u, 0xBB99u);
 }
 
+// Keep bits of 32 consecutive elements from block `blk`: bit 4 b + j is
+// element 8 b + 2 j, bit 16 + 4 b + j element 8 b + 2 j + 1.
+__device__ __forceinline__ uint32_t drop_bits32(const DropParams& d, uint2 off, uint64_t blk) {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        uint32_t m[4];
+        drop_mask8(d, off, blk + b, m);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) bits |= m[j] & (0x00010001u << (4 * b + j));
+    }
+    return bits;
+}
+
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
@@ -152,60 +166,6 @@ __global__ void __launch_bounds__(256) k_dropout(const T* X, T* Y, int64_t n, co
                     keep ? (uint16_t)(pack_bf16x2(__fmul_rn(x, d.up), 0.0f) & 0xFFFFu) : (uint16_t)0;
             }
         }
-    }
-}
-
-// ---------------------------------------------------------------------------
-// Adapter dropout of the linear: masked copy of X for the adapter GEMMs, and
-// the masked adapter term of dX.
-// ---------------------------------------------------------------------------
-// Xd = X where kept, else +0 (unscaled: the factor goes into the adapter's
-// scale, so that the masked bf16 values stay exact); n8 blocks of eight.
-__global__ void __launch_bounds__(256) k_drop_mask(const uint4* X, uint4* Xd, int64_t n8,
-                                                   const __grid_constant__ DropParams d) {
-    pdl_trigger();
-    pdl_wait();
-    const uint2 off = drop_offset(d);
-    for (int64_t b = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; b < n8; b += (int64_t)gridDim.x * blockDim.x) {
-        uint32_t m[4];
-        drop_mask8(d, off, (uint64_t)b, m);
-        const uint4 v = X[b];
-        Xd[b] = make_uint4(v.x & m[0], v.y & m[1], v.z & m[2], v.w & m[3]);
-    }
-}
-
-// dX[m][k] += kept(m K + k) * sum_j G[m][j] A[j][k], eight columns a thread.
-__global__ void __launch_bounds__(256) k_lora_dx_masked(uint4* dX, const uint16_t* G, const uint16_t* A, int64_t M,
-                                                        int64_t K, int rt, const __grid_constant__ DropParams d) {
-    pdl_trigger();
-    pdl_wait();
-    const uint2 off = drop_offset(d);
-    const int64_t k8 = K / 8;
-    for (int64_t b = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; b < M * k8;
-         b += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t m = b / k8, c = b - m * k8;
-        float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (int j = 0; j < rt; ++j) {
-            const float g = bf16_lo(G[m * rt + j]);
-            const uint4 a = *reinterpret_cast<const uint4*>(A + (int64_t)j * K + c * 8);
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                acc[2 * q] = fmaf(g, bf16_lo(w[q]), acc[2 * q]);
-                acc[2 * q + 1] = fmaf(g, bf16_hi(w[q]), acc[2 * q + 1]);
-            }
-        }
-        uint32_t mk[4];
-        drop_mask8(d, off, (uint64_t)b, mk);
-        const uint4 v = dX[b];
-        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-        uint32_t o[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const uint32_t sum = pack_bf16x2(bf16_lo(x[q]) + acc[2 * q], bf16_hi(x[q]) + acc[2 * q + 1]);
-            o[q] = (sum & mk[q]) | (x[q] & ~mk[q]);
-        }
-        dX[b] = make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 

@@ -22,6 +22,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "dropout.cuh"
 #include "internal.h"
 #include "nf4.cuh"
 
@@ -68,6 +69,8 @@ struct GemmParams {
     // the map of the kept pre-activations [M][2F] where keep_gu
     int gate_rows, act, keep_gu;
     CUtensorMap tmGU;
+    // dropout form of the pair dX kernel: the mask of the adapter's term
+    DropParams dp;
 };
 
 // First sU column of the adapter of the output rows starting at n0.

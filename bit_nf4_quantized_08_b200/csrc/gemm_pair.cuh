@@ -112,10 +112,19 @@ struct PairSchedule {
 // k-steps over sU = [U_gate | U_up]: the leader's B tile starts at column 0 of
 // its adapter and its peer's at column -r, and the loads' zero fill to the
 // left and right makes the block-diagonal operand.
-template <int DQ, int STAGES, bool SK, bool GATED = false>
+//
+// DROP (dX under adapter dropout): the adapter's term sG A is masked, the base
+// term is not, and both sums share an accumulator (the two accumulators fill
+// TMEM).  So the LoRA k-steps run first; their sum is masked in TMEM by the
+// epilogue warps (load, select by the recomputed keep bits, store), and the
+// main k-steps accumulate onto it: one rounding, no traffic besides sG and A.
+// The keep bits of a thread's 512 elements (16 registers) are generated while
+// the first operands are on their way.
+template <int DQ, int STAGES, bool SK, bool GATED = false, bool DROP = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREADS, 1)
     k_gemm_pair(const __grid_constant__ GemmParams p) {
     static_assert(!GATED || (DQ == DQ_B_K && !SK), "the gated form is a forward on the grid schedule");
+    static_assert(!DROP || (DQ == DQ_B_MN && !SK), "the dropout form is a dX GEMM on the grid schedule");
     using S = PairShape<DQ>;
     constexpr int B_MN = DQ == DQ_B_MN ? 1 : 0;
     extern __shared__ uint8_t smem_raw[];
@@ -137,6 +146,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREA
         reinterpret_cast<uint32_t*>(gbase + S::STAGE_BYTES * STAGES + 8 * (3 * STAGES + 2 + PF_SLOTS));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     volatile int* epi_skip = reinterpret_cast<volatile int*>(tmem_holder + 2);  // [2]
+    const uint32_t lora_full = bar_base + 8u * (3 * STAGES + 2 + PF_SLOTS + 2);  // DROP: the adapter's sums are complete
+    const uint32_t lora_done = lora_full + 8u;                                   // DROP: and masked
+    static_assert(8 * (3 * STAGES + 2 + PF_SLOTS + 4) <= 256, "barriers");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -151,6 +163,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREA
         mbar_init(acc_full, 1);
         mbar_init(acc_empty, 2 * S::NDQ_WARPS);  // epilogue warps of both CTAs (leader's copy is used)
         for (int j = 0; j < PF_SLOTS; ++j) mbar_init(pf_full(j), 1);
+        if (DROP) {
+            mbar_init(lora_full, 1);
+            mbar_init(lora_done, 2 * S::NDQ_WARPS);
+        }
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -190,7 +206,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREA
                 const int nb0 = GATED ? sg.tn * 128 + (int)rank * p.gate_rows : sg.tn * 256 + 128 * (int)rank;
                 for (int k = sg.k0; k < sg.k1; ++k, ++it) {
                     const int s = it % STAGES, u = it / STAGES;
-                    if (k >= p.ks_main && !waited) {
+                    const bool lora = DROP ? k < p.ks_lora : k >= p.ks_main;
+                    if (lora && !waited) {
                         pdl_wait();
                         waited = true;
                     }
@@ -199,8 +216,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREA
                     const uint32_t sB = sA + S::A_BYTES;
                     const uint32_t sC = sB + S::B_BYTES;
                     const uint32_t sS = sC + S::CODE_BYTES;
-                    const bool lora = k >= p.ks_main;
-                    const int kc = lora ? k - p.ks_main : k;
+                    const int kc = DROP ? (lora ? k : k - p.ks_lora) : (lora ? k - p.ks_main : k);
                     uint32_t bytes = S::A_BYTES;
                     if (lora) {
                         bytes += S::B_BYTES;
@@ -280,6 +296,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREA
                         }
                     }
                     umma_commit_pair_mc(empty(s), 0x3);
+                    if (DROP && k == p.ks_lora - 1) {
+                        umma_commit_pair_mc(lora_full, 0x3);
+                        if (!mbar_wait(lora_done, 0, wc)) { ok = false; *abort_flag = 1; break; }
+                        tc_fence_after();
+                    }
                 }
                 // one acc_full phase per segment, also when it was cut short
                 umma_commit_pair_mc(acc_full, 0x3);
@@ -319,9 +340,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREA
         // but still walks every segment, so that the four epilogue warps
         // reach the same named barriers in the same order.
         bool dead = false;
+        uint32_t keep[DROP ? 16 : 1];
         while (sch.next(p, sg)) {
             const int m0 = sg.tm * 512, n0 = sg.tn * 256;
             const int nb0 = n0 + 128 * (int)rank;
+            if (DROP) {
+                // (whatever wrote the offset's device counter completed before
+                // the kernel ahead let this one start)
+                const uint2 off = drop_offset(p.dp);
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt) {
+                    const int64_t e = (int64_t)(m0 + 256 * mt + 128 * (int)rank + row) * p.cols + n0;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) keep[(DROP ? mt * 8 + c : 0)] = drop_bits32(p.dp, off, (uint64_t)(e >> 3) + 4 * c);
+                }
+            }
             for (int k = sg.k0; k < sg.k1; ++k, ++it) {
                 const int s = it % STAGES, u = it / STAGES;
                 if (dead) continue;
@@ -330,12 +363,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREA
                     dead = true;
                     continue;
                 }
-                if (k < p.ks_main) {
+                if (DROP ? k >= p.ks_lora : k < p.ks_main) {
                     const uint32_t st = base + s * S::STAGE_BYTES;
                     const uint32_t sOut = st + S::A_BYTES;
                     const uint32_t sC = sOut + S::B_BYTES;
+                    const int kc = DROP ? k - p.ks_lora : k;
                     const bool valid = DQ == DQ_B_MN
-                                           ? (64 * k + wrow < p.dq_rows) && (nb0 / 64 + kb_off < p.dq_kbs)
+                                           ? (64 * kc + wrow < p.dq_rows) && (nb0 / 64 + kb_off < p.dq_kbs)
                                            : true;
                     if (valid) {
                         const float a = ld_shared_f32(sC + S::CODE_BYTES + 4u * scale_idx);
@@ -357,6 +391,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREA
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(mapa_shared(full_dq(s), 0));
+                if (DROP && k == p.ks_lora - 1) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(lora_full, 0, wc))) {
+                        *abort_flag = 1;
+                        dead = true;
+                        continue;
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int i = 0; i < (DROP ? 16 : 0); ++i) {
+                        const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(i * 32);
+                        uint32_t v[32];
+                        tmem_ld_32x32b_x32(ta, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!(keep[DROP ? i : 0] & (1u << ((e >> 1) + 16 * (e & 1))))) v[e] = 0u;
+                        tmem_st_32x32b_x32(ta, v);
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(mapa_shared(lora_done, 0));
+                }
             }
 
             // -------------------------------------------------------- epilogue of the segment

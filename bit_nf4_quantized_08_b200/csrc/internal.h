@@ -73,13 +73,11 @@ struct LinearArgs {
     const qlora_nf4_weight* w;
     int nseg;
     int64_t seg_rows;
-    // adapter dropout (null: none), and what the adapter reads in place of X
-    // then; scale already holds the factor of the kept elements
+    // adapter dropout (null: none); scale already holds the factor of the
+    // kept elements
     const struct DropParams* drop;
-    const void* Xd;
     int grad_bf16;  // dA and dB in bf16 instead of fp32
     int rt() const { return r * nseg; }  // columns of sU and sG
-    const void* adapter_in(const void* X) const { return Xd ? Xd : X; }
 };
 qlora_status linear_fwd_impl(const void* X, const LinearArgs& a, const void* A, const void* B,
                              void* Y, void* ws, size_t ws_bytes, cudaStream_t s);

@@ -123,8 +123,9 @@ inline int skinny_active_clusters(int cs) {
     return n;
 }
 
-template <int BN>
+template <int BN, bool DROP>
 inline cudaError_t launch_skinny(SkinnyParams& p, int tiles, int kmin, int kmax, cudaStream_t s) {
+    constexpr int threads = SkinnyShape<BN>::THREADS + (DROP ? 32 * (kMaskWarps - 4) : 0);
     constexpr int smem = SkinnyShape<BN>::SMEM;
     static_assert(smem <= 232448, "shared memory per CTA");
     // Cluster size: fewest rounds of resident clusters times k-steps per CTA
@@ -148,26 +149,25 @@ inline cudaError_t launch_skinny(SkinnyParams& p, int tiles, int kmin, int kmax,
     }
     for (int i = 0; i < p.nprob; ++i) p.pr[i].per = ceil_div(p.pr[i].ksteps, cs);
     p.total_tiles = tiles;
-    auto kern = k_skinny<BN>;
+    auto kern = k_skinny<BN, DROP>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     ProfileScope ps(QLORA_KERNEL_LORA_GEMM, s);
     note_launch();
     if (p.pack)  // two independent tiles per cluster of 2: one TPC each
-        return launch_pdl(kern, dim3((unsigned)((tiles + 1) & ~1), 1, 1), dim3(SkinnyShape<BN>::THREADS, 1, 1), smem,
-                          s, 2, p);
-    return launch_pdl(kern, dim3((unsigned)(tiles * cs), 1, 1), dim3(SkinnyShape<BN>::THREADS, 1, 1), smem, s, cs,
-                      p);
+        return launch_pdl(kern, dim3((unsigned)((tiles + 1) & ~1), 1, 1), dim3(threads, 1, 1), smem, s, 2, p);
+    return launch_pdl(kern, dim3((unsigned)(tiles * cs), 1, 1), dim3(threads, 1, 1), smem, s, cs, p);
 }
 
-template <int BN>
+template <int BN, bool DROP>
 inline cudaError_t launch_lora_stream(SkinnyParams& p, int tiles, int nctas, cudaStream_t s) {
     constexpr int smem = StreamShape<BN>::SMEM;
     static_assert(smem <= 232448, "shared memory per CTA");
     for (int i = 0; i < p.nprob; ++i) p.pr[i].per = p.pr[i].ksteps;
     p.total_tiles = tiles;
     p.pack = 0;
-    auto kern = k_lora_stream<BN>;
+    constexpr int threads = StreamShape<BN>::THREADS + (DROP ? 32 * kMaskWarps : 0);
+    auto kern = k_lora_stream<BN, DROP>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     ProfileScope ps(QLORA_KERNEL_LORA_GEMM, s);
@@ -175,7 +175,7 @@ inline cudaError_t launch_lora_stream(SkinnyParams& p, int tiles, int nctas, cud
     // clusters of 2 only for placement (the CTAs are independent): whole
     // TPCs, never one SM of a TPC that a CTA-pair kernel beside it could use
     const int grid = (std::max(1, std::min(tiles, nctas)) + 1) & ~1;
-    return launch_pdl(kern, dim3((unsigned)grid, 1, 1), dim3(StreamShape<BN>::THREADS, 1, 1), smem, s, 2, p);
+    return launch_pdl(kern, dim3((unsigned)grid, 1, 1), dim3(threads, 1, 1), smem, s, 2, p);
 }
 
 // One skinny problem: operands (tensor maps and majorness), extent and output.
@@ -189,6 +189,8 @@ struct SkinnyDesc {
     int64_t out_ld;
     int r;         // output columns (0: the launch's r)
     int seg_mode, seg_rows, seg_r;  // SK_SEG_* (fused projections)
+    const DropParams* drop;  // the A operand is X under this dropout, or null
+    int64_t drop_cols;       // X's row length
 };
 
 // wait_first: the operands may have been written by the kernel just before on
@@ -199,6 +201,19 @@ struct SkinnyDesc {
 // persistent kernel on up to nctas CTAs: work beside a kernel that holds
 // most SMs; with ctrs the CTAs take tiles from a shared counter).
 enum { SKP_SPLIT = 0, SKP_PACKED = 1, SKP_STREAM = 2 };
+template <bool DROP>
+inline cudaError_t launch_lora(SkinnyParams& p, int bn, int place, int tiles, int kmin, int kmax, int nctas,
+                               cudaStream_t s) {
+    if (place == SKP_STREAM) {
+        if (bn == 64) return launch_lora_stream<64, DROP>(p, tiles, nctas, s);
+        if (bn == 128) return launch_lora_stream<128, DROP>(p, tiles, nctas, s);
+        return launch_lora_stream<256, DROP>(p, tiles, nctas, s);
+    }
+    if (bn == 64) return launch_skinny<64, DROP>(p, tiles, kmin, kmax, s);
+    if (bn == 128) return launch_skinny<128, DROP>(p, tiles, kmin, kmax, s);
+    return launch_skinny<256, DROP>(p, tiles, kmin, kmax, s);
+}
+
 // SKP_STREAM with ctrs (two ints, zero before the launch): tiles taken in
 // problem order from ctrs[0]; problem dep_prob reads problem 0's output.
 // wait_mask (SKP_STREAM with wait_first == 0): problems that read the
@@ -237,27 +252,19 @@ inline qlora_status skinny(const SkinnyDesc* d, int nprob, int r, cudaStream_t s
         q.out_mode = d[i].out_mode;
         q.out = d[i].out;
         q.out_ld = d[i].out_ld;
+        if (d[i].drop) {  // (one dropout a launch: every masked problem reads the same X)
+            q.drop = 1;
+            p.dp = *d[i].drop;
+            p.drop_cols = d[i].drop_cols;
+        }
     }
     p.nprob = nprob;
     p.timeout_ns = wait_timeout_ns();
     p.inject = inject_mode() == 1 ? 1 : 0;
-    const int bn = lora_bn(r);
-    cudaError_t e;
-    if (place == SKP_STREAM) {
-        if (bn == 64)
-            e = launch_lora_stream<64>(p, tiles, nctas, s);
-        else if (bn == 128)
-            e = launch_lora_stream<128>(p, tiles, nctas, s);
-        else
-            e = launch_lora_stream<256>(p, tiles, nctas, s);
-        return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
-    }
-    if (bn == 64)
-        e = launch_skinny<64>(p, tiles, kmin, kmax, s);
-    else if (bn == 128)
-        e = launch_skinny<128>(p, tiles, kmin, kmax, s);
-    else
-        e = launch_skinny<256>(p, tiles, kmin, kmax, s);
+    bool drop = false;
+    for (int i = 0; i < nprob; ++i) drop = drop || p.pr[i].drop;
+    const cudaError_t e = drop ? launch_lora<true>(p, lora_bn(r), place, tiles, kmin, kmax, nctas, s)
+                               : launch_lora<false>(p, lora_bn(r), place, tiles, kmin, kmax, nctas, s);
     return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
@@ -339,13 +346,13 @@ inline size_t linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int r, int
 // Tile schedule of the dequant GEMMs: stream-K over a persistent grid of
 // one CTA per SM when there are at least two k-steps per CTA, else one CTA
 // per tile.  Debug mode 2 forces stream-K on 7 CTAs (tests of the merge).
-template <int DQ, int STAGES, bool GATED = false>
+template <int DQ, int STAGES, bool GATED = false, bool DROP = false>
 inline cudaError_t launch_gemm_pair(const GemmParams& p, dim3 grid, cudaStream_t s, int prof_kind) {
     constexpr int smem = pair_smem_bytes<DQ, STAGES>();
     static_assert(smem <= 232448, "shared memory per CTA");
-    auto kern = GATED       ? k_gemm_pair<DQ, STAGES, false, GATED>
-                : p.streamk ? k_gemm_pair<DQ, STAGES, true>
-                            : k_gemm_pair<DQ, STAGES, false>;
+    auto kern = GATED || DROP ? k_gemm_pair<DQ, STAGES, false, GATED, DROP>
+                : p.streamk   ? k_gemm_pair<DQ, STAGES, true>
+                              : k_gemm_pair<DQ, STAGES, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     ProfileScope ps(prof_kind, s);
@@ -467,7 +474,9 @@ inline bool map_codes(CUtensorMap* m, const qlora_nf4_weight& w, uint32_t box_by
 // (A = [A_0; A_1; ...] of a fused projection: every adapter's sU in one pass over X)
 inline bool desc_sU(SkinnyDesc* d, const void* X, const LinearArgs& a, const void* A, void* sU) {
     memset(d, 0, sizeof(*d));
-    if (!map_bf16(&d->tA, a.adapter_in(X), a.K, a.M, 128)) return false;
+    if (!map_bf16(&d->tA, X, a.K, a.M, 128)) return false;
+    d->drop = a.drop;
+    d->drop_cols = a.K;
     if (!map_bf16(&d->tB, A, a.K, a.rt(), lora_bn(a.rt()))) return false;
     d->rows = (int)a.M;
     d->ksteps = (int)(a.K / 64);
@@ -774,7 +783,9 @@ inline bool desc_sG(SkinnyDesc* d, const CUtensorMap& tdY, const LinearArgs& a, 
 inline bool desc_dA_dB(SkinnyDesc* d, const void* dY, const void* X, const LinearArgs& a, const LinearWs& L,
                        void* dA, void* dB) {
     memset(d, 0, 2 * sizeof(*d));
-    if (!map_bf16(&d[0].tA, a.adapter_in(X), a.K, a.M, 64)) return false;
+    if (!map_bf16(&d[0].tA, X, a.K, a.M, 64)) return false;
+    d[0].drop = a.drop;
+    d[0].drop_cols = a.K;
     if (!map_bf16(&d[0].tB, L.sG, a.rt(), a.M, 64)) return false;
     d[0].rows = (int)a.K;
     d[0].out_mode = a.grad_bf16 ? SK_OUT_BF16_T : SK_OUT_F32_T;
@@ -812,8 +823,7 @@ inline qlora_status launch_dx_gemm(const void* A, void* dX, const LinearArgs& a,
     p.tmA = tdY;
     p.tmB = tdY;
     if (!map_codes(&p.tmCodes, w, 128, 64)) return QLORA_ERR_CUDA;
-    const bool lora = a.r > 0 && !a.drop;  // with dropout the adapter term is masked and added apart
-    if (lora) {
+    if (a.r > 0) {
         if (!map_bf16(&p.tmA2, L.sG, a.rt(), a.M, 128)) return QLORA_ERR_CUDA;
         if (!map_bf16(&p.tmB2, A, a.K, a.rt(), 64)) return QLORA_ERR_CUDA;
     } else {
@@ -826,7 +836,7 @@ inline qlora_status launch_dx_gemm(const void* A, void* dX, const LinearArgs& a,
     p.dq_rows = (int)a.N;
     p.dq_kbs = (int)(a.K / 64);
     p.ks_main = ceil_div(a.N, 64);
-    p.ks_lora = lora ? ceil_div(a.rt(), 64) : 0;
+    p.ks_lora = a.r > 0 ? ceil_div(a.rt(), 64) : 0;
     p.ks_per_split = p.ks_main;
     p.rows = (int)a.M;
     p.cols = (int)a.K;
@@ -835,7 +845,15 @@ inline qlora_status launch_dx_gemm(const void* A, void* dX, const LinearArgs& a,
     if (!map_bf16(&p.tmOut, dX, a.K, a.M, 128)) return QLORA_ERR_CUDA;
     p.timeout_ns = wait_timeout_ns();
     p.inject = inject_mode() == 1 ? 1 : 0;
-    if (large_m_schedule() == SCHED_PAIR || large_m_schedule() == SCHED_PAIR_SK) {
+    if (a.drop) {
+        // the adapter's k-steps come first, so sG is waited for at the start;
+        // one pair per tile whatever schedule the linears use
+        if (!map_codes(&p.tmCodes, w, 64, 64)) return QLORA_ERR_CUDA;
+        p.dp = *a.drop;
+        const dim3 grid = grid_pair(p, ceil_div(a.K, 256), ceil_div(a.M, 512));
+        if (launch_gemm_pair<DQ_B_MN, 4, false, true>(p, grid, s, QLORA_KERNEL_DX_GEMM) != cudaSuccess)
+            return QLORA_ERR_CUDA;
+    } else if (large_m_schedule() == SCHED_PAIR || large_m_schedule() == SCHED_PAIR_SK) {
         if (!map_codes(&p.tmCodes, w, 64, 64)) return QLORA_ERR_CUDA;
         p.late_wait = late_wait;
         dim3 grid = schedule_pair<DQ_B_MN, 4>(p, ceil_div(a.K, 256), ceil_div(a.M, 512), L);
@@ -866,16 +884,6 @@ inline cudaError_t launch_dropout(const void* X, bool is_bf16, int64_t n, const 
                       static_cast<float*>(Y), n, d);
 }
 
-// dX += keep * (sG A)
-inline qlora_status launch_lora_dx_masked(const void* A, void* dX, const LinearArgs& a, const LinearWs& L,
-                                          cudaStream_t s) {
-    note_launch();
-    const cudaError_t e = launch_pdl(k_lora_dx_masked, dim3(elementwise_grid(a.M * a.K / 8)), dim3(256), 0, s, 0,
-                                     static_cast<uint4*>(dX), (const uint16_t*)L.sG, static_cast<const uint16_t*>(A),
-                                     a.M, a.K, a.rt(), *a.drop);
-    return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
-}
-
 // The backward forks its adapter GEMMs onto the side stream when the dX GEMM
 // runs on the CTA-pair kernel, one pair per tile.
 inline bool side_fork_ok() { return large_m_schedule() == SCHED_PAIR; }
@@ -892,13 +900,13 @@ inline qlora_status linear_bwd_forked(const void* dY, const void* X, const Linea
                                       const CUtensorMap& tdY, const SideStream& side, cudaStream_t s) {
     SkinnyDesc dg;
     if (!desc_sG(&dg, tdY, a, B, L.sG)) return QLORA_ERR_CUDA;
-    qlora_status st = skinny(&dg, 1, a.rt(), s, 1, SKP_PACKED);
+    // (under dropout the dX GEMM needs sG first: over the whole GPU instead)
+    qlora_status st = skinny(&dg, 1, a.rt(), s, 1, a.drop ? SKP_SPLIT : SKP_PACKED);
     if (st != QLORA_OK) return st;
     if (cudaEventRecord(side.fork, s) != cudaSuccess) return QLORA_ERR_CUDA;
     if (cudaStreamWaitEvent(side.st, side.fork, 0) != cudaSuccess) return QLORA_ERR_CUDA;
     // from here on the side stream is joined back whatever happens
-    st = launch_dx_gemm(A, dX, a, L, tdY, a.drop ? 0 : 1, s);
-    if (st == QLORA_OK && a.drop) st = launch_lora_dx_masked(A, dX, a, L, s);
+    st = launch_dx_gemm(A, dX, a, L, tdY, 1, s);
     // sU, dA and dB in one persistent launch over every SM: the CTAs that
     // find an SM beside the GEMM take tiles from the shared counter while it
     // runs, the rest start as it ends.  sU tiles (inputs only) start at once,
@@ -954,7 +962,6 @@ inline qlora_status linear_bwd_impl(const void* dY, const void* X, const LinearA
     }
     if (dX) {
         qlora_status st = launch_dx_gemm(A, dX, a, L, tdY, 0, s);
-        if (st == QLORA_OK && a.drop) st = launch_lora_dx_masked(A, dX, a, L, s);
         if (st != QLORA_OK) return st;
     }
     if (a.r > 0) {
@@ -969,14 +976,13 @@ inline qlora_status linear_bwd_impl(const void* dY, const void* X, const LinearA
 
 // ---------------------------------------------------------------------------
 // Adapter dropout and the gated feed-forward on the linear's forward and
-// backward.  Workspace: the linear's, then the masked X (dropout), then the
-// pre-activations [M, 2F] the caller does not keep (gated forward) or their
-// gradient (gated backward).
+// backward.  Workspace: the linear's, then the pre-activations [M, 2F] that
+// the caller does not keep (gated forward, few tokens) or their gradient
+// (gated backward).
 // ---------------------------------------------------------------------------
 struct BlockWs {
     void* linear;
     size_t linear_bytes;
-    void* Xd;
     uint16_t* gu;
     size_t bytes;
 };
@@ -986,49 +992,17 @@ inline BlockWs carve_block_ws(void* ws, int64_t M, int64_t N, int64_t K, int rt,
     b.linear_bytes = linear_workspace_bytes(M, N, K, rt, bwd);
     WsCarve c{static_cast<char*>(ws), 0};
     b.linear = c.take(b.linear_bytes);
-    b.Xd = rt > 0 ? c.take((size_t)M * K * 2) : nullptr;
     b.gu = gated && (bwd || M <= kSmallM) ? static_cast<uint16_t*>(c.take((size_t)M * N * 2)) : nullptr;
     b.bytes = c.used;
     return b;
 }
 
-// The adapter's input under dropout: X where kept, else 0.
-inline qlora_status mask_input(const void* X, LinearArgs& a, const BlockWs& b, cudaStream_t s) {
-    if (!a.drop) return QLORA_OK;
-    a.Xd = b.Xd;
-    note_launch();
-    const int64_t n8 = a.M * a.K / 8;
-    const cudaError_t e = launch_pdl(k_drop_mask, dim3(elementwise_grid(n8)), dim3(256), 0, s, 0,
-                                     static_cast<const uint4*>(X), static_cast<uint4*>(b.Xd), n8, *a.drop);
-    return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
-}
-
-inline qlora_status dropout_fwd_impl(const void* X, LinearArgs a, const void* A, const void* B, void* Y, void* ws,
-                                     cudaStream_t s) {
-    const BlockWs b = carve_block_ws(ws, a.M, a.N, a.K, a.rt(), 0, 0);
-    qlora_status st = mask_input(X, a, b, s);
-    if (st != QLORA_OK) return st;
-    return linear_fwd_impl(X, a, A, B, Y, b.linear, b.linear_bytes, s);
-}
-
-inline qlora_status dropout_bwd_impl(const void* dY, const void* X, LinearArgs a, const void* A, const void* B,
-                                     void* dX, void* dA, void* dB, void* ws, cudaStream_t s) {
-    const BlockWs b = carve_block_ws(ws, a.M, a.N, a.K, a.rt(), 1, 0);
-    if (a.M > 0) {
-        qlora_status st = mask_input(X, a, b, s);
-        if (st != QLORA_OK) return st;
-    }
-    return linear_bwd_impl(dY, X, a, A, B, dX, dA, dB, b.linear, b.linear_bytes, s);
-}
-
-inline qlora_status gated_fwd_impl(const void* X, LinearArgs a, const void* A, const void* B, int act, void* H,
-                                   void* GU, void* ws, cudaStream_t s) {
+inline qlora_status gated_fwd_impl(const void* X, const LinearArgs& a, const void* A, const void* B, int act,
+                                   void* H, void* GU, void* ws, cudaStream_t s) {
     const BlockWs b = carve_block_ws(ws, a.M, a.N, a.K, a.rt(), 0, 1);
-    qlora_status st = mask_input(X, a, b, s);
-    if (st != QLORA_OK) return st;
     if (a.M > kSmallM) return gated_fwd_large(X, a, A, B, act, H, GU, b.linear, s);
     uint16_t* gu = GU ? static_cast<uint16_t*>(GU) : b.gu;
-    st = linear_fwd_impl(X, a, A, B, gu, b.linear, b.linear_bytes, s);
+    const qlora_status st = linear_fwd_impl(X, a, A, B, gu, b.linear, b.linear_bytes, s);
     if (st != QLORA_OK) return st;
     note_launch();
     const cudaError_t e = launch_pdl(k_gated_act, dim3(elementwise_grid(a.M * a.seg_rows / 8)), dim3(256), 0, s, 0,
@@ -1036,12 +1010,10 @@ inline qlora_status gated_fwd_impl(const void* X, LinearArgs a, const void* A, c
     return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
-inline qlora_status gated_bwd_impl(const void* dH, const void* X, const void* GU, LinearArgs a, const void* A,
+inline qlora_status gated_bwd_impl(const void* dH, const void* X, const void* GU, const LinearArgs& a, const void* A,
                                    const void* B, int act, void* dX, void* dA, void* dB, void* ws, cudaStream_t s) {
     const BlockWs b = carve_block_ws(ws, a.M, a.N, a.K, a.rt(), 1, 1);
     if (a.M > 0) {
-        qlora_status st = mask_input(X, a, b, s);
-        if (st != QLORA_OK) return st;
         note_launch();
         const cudaError_t e = launch_pdl(k_gated_grad, dim3(elementwise_grid(a.M * a.seg_rows / 8)), dim3(256), 0, s,
                                          0, static_cast<const uint16_t*>(dH), static_cast<const uint16_t*>(GU), b.gu,

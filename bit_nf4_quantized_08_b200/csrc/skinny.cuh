@@ -18,6 +18,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "dropout.cuh"
 #include "gemm.cuh"
 
 namespace qlora {
@@ -44,6 +45,7 @@ struct SkinnyProblem {
     // (dB of a segment reads its own sU columns).  Shifted-out columns read
     // the load's zero fill.
     int seg_mode, seg_rows, seg_r;
+    int drop;  // the A operand is X under dropout: masked in shared memory (DROP kernels)
 };
 
 enum { SK_SEG_NONE = 0, SK_SEG_REDUCE = 1, SK_SEG_ROWS = 2 };
@@ -77,7 +79,42 @@ struct SkinnyParams {
     // operands come from the previous kernel; the producer waits for it
     // before the first such tile only
     int wait_mask;
+    DropParams dp;     // dropout of X (DROP kernels)
+    int64_t drop_cols;  // X's row length
 };
+
+// Adapter dropout: the A tiles of X pass through mask warps between their TMA
+// load and the MMA.  A tile is 128 lines of 64 consecutive elements of X
+// (K-major: a token row each; MN-major: 64 tokens of each of two 64-column
+// chunks), eight generator blocks a line.  Thread t of the 256 takes half of
+// line t % 128: its four blocks' masks, each ANDed onto one 16-byte chunk of
+// the 128-byte-swizzled line (eight neighbouring lines give eight different
+// chunks, so the accesses are free of bank conflicts).  The generator, about
+// 55 instructions a block, sets the pace: with eight warps about 300 cycles a
+// tile, near the time a tile takes to arrive.
+constexpr int kMaskWarps = 8;
+
+// Element index of the first element of line l of the A tile of rows m0.. at k-step k.
+__device__ __forceinline__ int64_t drop_line(const SkinnyProblem& P, int64_t cols, int m0, int k, int l) {
+    return P.a_mn ? (int64_t)(k * 64 + (l & 63)) * cols + m0 + (l & ~63)
+                  : (int64_t)(m0 + l) * cols + (int64_t)k * 64;
+}
+
+// Masks the tile at shared address sA (t: 0..255).
+__device__ __forceinline__ void drop_tile(const SkinnyProblem& P, const DropParams& d, uint2 off, int64_t cols, int m0,
+                                          int k, uint32_t sA, int t) {
+    const int l = t & 127, q0 = (t >> 7) * 4;
+    const uint64_t blk = (uint64_t)(drop_line(P, cols, m0, k, l) >> 3) + q0;
+    uint32_t m[4][4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) drop_mask8(d, off, blk + q, m[q]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t a = sA + (uint32_t)l * 128u + (uint32_t)(((q0 + q) ^ (l & 7)) << 4);
+        const uint4 v = ld_shared_v4(a);
+        st_shared_v4(a, v.x & m[q][0], v.y & m[q][1], v.z & m[q][2], v.w & m[q][3]);
+    }
+}
 
 template <int BN>
 struct SkinnyShape {
@@ -116,8 +153,9 @@ __device__ __forceinline__ void st_async_v4(uint32_t addr, uint32_t a, uint32_t 
         : "memory");
 }
 
-template <int BN>
-__global__ void __launch_bounds__(SkinnyShape<BN>::THREADS, 1) k_skinny(const __grid_constant__ SkinnyParams p) {
+template <int BN, bool DROP = false>
+__global__ void __launch_bounds__(SkinnyShape<BN>::THREADS + (DROP ? 32 * (kMaskWarps - 4) : 0), 1)
+    k_skinny(const __grid_constant__ SkinnyParams p) {
     using S = SkinnyShape<BN>;
     constexpr int STAGES = S::STAGES;
     extern __shared__ uint8_t smem_raw[];
@@ -130,7 +168,9 @@ __global__ void __launch_bounds__(SkinnyShape<BN>::THREADS, 1) k_skinny(const __
     auto empty = [&](int s) { return bar_base + 8u * (STAGES + s); };
     const uint32_t acc_full = bar_base + 8u * (2 * STAGES);
     const uint32_t red_full = bar_base + 8u * (2 * STAGES + 1);
+    auto masked = [&](int s) { return bar_base + 8u * (2 * STAGES + 3 + s); };  // DROP: tile masked
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(gbase + S::REGION + 8 * (2 * STAGES + 2));
+    static_assert(8 * (3 * STAGES + 3) <= 256, "barriers");
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -156,6 +196,8 @@ __global__ void __launch_bounds__(SkinnyShape<BN>::THREADS, 1) k_skinny(const __
             mbar_init(full(s), 1);
             mbar_init(empty(s), 1);
         }
+        if (DROP)
+            for (int s = 0; s < STAGES; ++s) mbar_init(masked(s), kMaskWarps);
         mbar_init(acc_full, 1);
         mbar_init(red_full, 1);
         // every rank (this one included) sends rows_per rows of rc floats here
@@ -217,9 +259,10 @@ __global__ void __launch_bounds__(SkinnyShape<BN>::THREADS, 1) k_skinny(const __
     } else if (warp == 1) {
         if (lane == 0) {
             const uint32_t idesc = idesc_bf16_f32(128, BN, a_mn, b_mn);
+            const bool drop = DROP && P.drop;
             for (int i = 0; i < nk; ++i) {
                 const int s = i % STAGES, u = i / STAGES;
-                if (!mbar_wait(full(s), u & 1, wc)) { *abort_flag = 1; break; }
+                if (!mbar_wait(drop ? masked(s) : full(s), u & 1, wc)) { *abort_flag = 1; break; }
                 tc_fence_after();
                 const uint32_t sA = base + s * S::STAGE_BYTES;
                 const uint32_t sB = sA + S::A_BYTES;
@@ -240,8 +283,22 @@ __global__ void __launch_bounds__(SkinnyShape<BN>::THREADS, 1) k_skinny(const __
         }
     }
 
-    if (warp < 2) {
-        // producer and MMA warps: nothing left but the two cluster barriers
+    if (DROP && warp >= 2 && P.drop) {
+        // ------------------------------------------------------------ mask warps (the epilogue's and four more)
+        if (p.wait_first) pdl_wait();  // the offset's device counter
+        const uint2 off = drop_offset(p.dp);
+        for (int i = 0; i < nk; ++i) {
+            const int s = i % STAGES, u = i / STAGES;
+            if (!__all_sync(0xffffffffu, mbar_wait(full(s), u & 1, wc))) { *abort_flag = 1; break; }
+            drop_tile(P, p.dp, off, p.drop_cols, m0, k0 + i, base + s * S::STAGE_BYTES, (int)threadIdx.x - 64);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(masked(s));
+        }
+    }
+
+    if (warp < 2 || warp >= 6) {
+        // producer, MMA and spare mask warps: nothing left but the two cluster barriers
         if (S::RED_OVERLAY) cluster_arrive();
         cluster_wait();
         cluster_arrive();
@@ -373,8 +430,9 @@ struct StreamShape {
     static constexpr int TMEM_COLS = 2 * BN;
 };
 
-template <int BN>
-__global__ void __launch_bounds__(StreamShape<BN>::THREADS, 1) k_lora_stream(const __grid_constant__ SkinnyParams p) {
+template <int BN, bool DROP = false>
+__global__ void __launch_bounds__(StreamShape<BN>::THREADS + (DROP ? 32 * kMaskWarps : 0), 1)
+    k_lora_stream(const __grid_constant__ SkinnyParams p) {
     using S = StreamShape<BN>;
     constexpr int STAGES = S::STAGES;
     constexpr int RING = 4;  // tile indices handed from the producer to the MMA and epilogue warps
@@ -392,6 +450,10 @@ __global__ void __launch_bounds__(StreamShape<BN>::THREADS, 1) k_lora_stream(con
     int* ring = reinterpret_cast<int*>(gbase + S::PIPE_BYTES + 8 * (2 * STAGES + 4 + 2 * RING));
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(ring + RING);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+    // DROP: the k-step's A tile is ready for the MMA (masked, or not X's)
+    constexpr int MASKED_OFF = 8 * (2 * STAGES + 4 + 2 * RING) + 4 * RING + 8;
+    static_assert(MASKED_OFF % 8 == 0 && MASKED_OFF + 8 * STAGES <= 512, "barriers");
+    auto masked = [&](int s) { return bar_base + (uint32_t)MASKED_OFF + 8u * s; };
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const WaitCfg wc{p.timeout_ns};
@@ -426,8 +488,10 @@ __global__ void __launch_bounds__(StreamShape<BN>::THREADS, 1) k_lora_stream(con
         }
         for (int j = 0; j < RING; ++j) {
             mbar_init(tile_full(j), 1);
-            mbar_init(tile_empty(j), 5);  // MMA thread + 4 epilogue warps
+            mbar_init(tile_empty(j), 5 + (DROP ? kMaskWarps : 0));  // MMA thread, 4 epilogue warps, mask warps
         }
+        if (DROP)
+            for (int s = 0; s < STAGES; ++s) mbar_init(masked(s), kMaskWarps);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -538,7 +602,7 @@ __global__ void __launch_bounds__(StreamShape<BN>::THREADS, 1) k_lora_stream(con
                 const uint32_t idesc = idesc_bf16_f32(128, BN, P.a_mn, P.b_mn);
                 for (int k = 0; ok && k < P.ksteps; ++k, ++it) {
                     const int s = it % STAGES, us = it / STAGES;
-                    if (!mbar_wait(full(s), us & 1, wc)) { *abort_flag = 1; ok = false; break; }
+                    if (!mbar_wait(DROP ? masked(s) : full(s), us & 1, wc)) { *abort_flag = 1; ok = false; break; }
                     tc_fence_after();
                     const uint32_t sA = base + s * S::STAGE_BYTES;
                     const uint32_t sB = sA + S::A_BYTES;
@@ -561,6 +625,37 @@ __global__ void __launch_bounds__(StreamShape<BN>::THREADS, 1) k_lora_stream(con
             }
             // the MMAs (and their reads of shared memory) are complete before the CTA exits
             if (last_buf >= 0) mbar_wait(acc_full(last_buf), last_use & 1, wc);
+        }
+    } else if (DROP && warp >= 6) {
+        // ------------------------------------------------------------ mask warps
+        // (whatever wrote the offset's device counter completed before the
+        // kernel ahead let this one start)
+        const uint2 off = drop_offset(p.dp);
+        bool ok = true;
+        int it = 0;
+        for (int li = 0; ok; ++li) {
+            const int t = take_tile(li, ok);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tile_empty(li % RING));
+            if (__any_sync(0xffffffffu, t < 0 || !ok)) break;
+            int pi, tile;
+            locate(t, pi, tile);
+            const SkinnyProblem& P = p.pr[pi];
+            for (int k = 0; k < P.ksteps; ++k, ++it) {
+                const int s = it % STAGES;
+                if (!__all_sync(0xffffffffu, mbar_wait(full(s), (it / STAGES) & 1, wc))) {
+                    *abort_flag = 1;
+                    ok = false;
+                    break;
+                }
+                if (P.drop) {
+                    drop_tile(P, p.dp, off, p.drop_cols, tile * 128, k, base + s * S::STAGE_BYTES,
+                              (int)threadIdx.x - 32 * 6);
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(masked(s));
+            }
         }
     } else {
         // ------------------------------------------------------------ epilogue: one row per thread
