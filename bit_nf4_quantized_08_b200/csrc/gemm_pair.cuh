@@ -115,13 +115,13 @@ struct PairSchedule {
 //
 // DROP (dX under adapter dropout): the adapter's term sG A is masked, the base
 // term is not, and both sums share an accumulator (the two accumulators fill
-// TMEM).  So the LoRA k-steps run first; their sum is masked in TMEM by the
-// epilogue warps (load, select by the recomputed keep bits, store), and the
-// main k-steps accumulate onto it: one rounding, no traffic besides sG and A.
-// The keep bits of a thread's 512 elements (16 registers) are generated while
-// the first operands are on their way.
+// TMEM).  So the LoRA k-steps run first; four more warps mask their sum in
+// TMEM (load, select by the recomputed keep bits, store), and the main k-steps
+// accumulate onto it: one rounding, no traffic besides sG and A.  The keep
+// bits of a thread's 512 elements (16 registers) are generated while the first
+// operands are on their way.
 template <int DQ, int STAGES, bool SK, bool GATED = false, bool DROP = false>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREADS + (DROP ? 128 : 0), 1)
     k_gemm_pair(const __grid_constant__ GemmParams p) {
     static_assert(!GATED || (DQ == DQ_B_K && !SK), "the gated form is a forward on the grid schedule");
     static_assert(!DROP || (DQ == DQ_B_MN && !SK), "the dropout form is a dX GEMM on the grid schedule");
@@ -309,6 +309,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREA
             // on an abort, nothing may still be in flight when the CTA exits
             if (!ok) mbar_wait(acc_full, (seg_i - 1) & 1, wc);
         }
+    } else if (DROP && warp >= 2 + S::NDQ_WARPS) {
+        // ------------------------------------------------------------ mask warps (both CTAs)
+        const int quarter = warp & 3;
+        PairSchedule<SK> sch(p);
+        PairSeg sg;
+        sch.next(p, sg);
+        // (whatever wrote the offset's device counter completed before the
+        // kernel ahead let this one start)
+        const uint2 off = drop_offset(p.dp);
+        uint32_t keep[16];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+            const int64_t m = sg.tm * 512 + 256 * mt + 128 * (int)rank + quarter * 32 + lane;
+            const uint64_t blk = (uint64_t)((m * p.cols + sg.tn * 256) >> 3);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) keep[mt * 8 + c] = drop_bits32(p.dp, off, blk + 4 * c);
+        }
+        if (__all_sync(0xffffffffu, mbar_wait(lora_full, 0, wc))) {
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(i * 32);
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(ta, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (!(keep[i] & (1u << ((e >> 1) + 16 * (e & 1))))) v[e] = 0u;
+                tmem_st_32x32b_x32(ta, v);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(lora_done, 0));
+        } else {
+            *abort_flag = 1;
+        }
     } else {
         // ------------------------------------------------------------ dequant + epilogue (both CTAs)
         const int ew = warp - 2;
@@ -340,21 +377,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREA
         // but still walks every segment, so that the four epilogue warps
         // reach the same named barriers in the same order.
         bool dead = false;
-        uint32_t keep[DROP ? 16 : 1];
         while (sch.next(p, sg)) {
             const int m0 = sg.tm * 512, n0 = sg.tn * 256;
             const int nb0 = n0 + 128 * (int)rank;
-            if (DROP) {
-                // (whatever wrote the offset's device counter completed before
-                // the kernel ahead let this one start)
-                const uint2 off = drop_offset(p.dp);
-#pragma unroll
-                for (int mt = 0; mt < 2; ++mt) {
-                    const int64_t e = (int64_t)(m0 + 256 * mt + 128 * (int)rank + row) * p.cols + n0;
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) keep[(DROP ? mt * 8 + c : 0)] = drop_bits32(p.dp, off, (uint64_t)(e >> 3) + 4 * c);
-                }
-            }
             for (int k = sg.k0; k < sg.k1; ++k, ++it) {
                 const int s = it % STAGES, u = it / STAGES;
                 if (dead) continue;
@@ -391,29 +416,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREA
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(mapa_shared(full_dq(s), 0));
-                if (DROP && k == p.ks_lora - 1) {
-                    if (!__all_sync(0xffffffffu, mbar_wait(lora_full, 0, wc))) {
-                        *abort_flag = 1;
-                        dead = true;
-                        continue;
-                    }
-                    tc_fence_after();
-#pragma unroll
-                    for (int i = 0; i < (DROP ? 16 : 0); ++i) {
-                        const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(i * 32);
-                        uint32_t v[32];
-                        tmem_ld_32x32b_x32(ta, v);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!(keep[DROP ? i : 0] & (1u << ((e >> 1) + 16 * (e & 1))))) v[e] = 0u;
-                        tmem_st_32x32b_x32(ta, v);
-                    }
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(mapa_shared(lora_done, 0));
-                }
             }
 
             // -------------------------------------------------------- epilogue of the segment
