@@ -19,9 +19,16 @@ namespace qlora {
 
 enum { ACT_SILU = 0, ACT_GELU_TANH = 1 };
 
-// 1 / (1 + exp(-x)), finite for every finite x: exp(-x) may overflow to
-// infinity, whose reciprocal is the right 0.
-__device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+// 1 / (1 + exp(-x)) with the hardware's base-2 exponential and reciprocal
+// (each within 2^-22 of the value; the results are rounded to 8 bits next).
+// Finite for every finite x: 2^y may overflow to infinity, whose reciprocal is
+// the right 0.
+__device__ __forceinline__ float sigmoid_f(float x) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 1.0f));
+    return r;
+}
 
 // act(g) and act'(g).
 __device__ __forceinline__ float act_value(int act, float g) {

@@ -17,6 +17,8 @@
 // uses cluster multicast.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "gated.cuh"
 #include "gemm.cuh"
@@ -121,7 +123,7 @@ struct PairSchedule {
 // bits of a thread's 512 elements (16 registers) are generated while the first
 // operands are on their way.
 template <int DQ, int STAGES, bool SK, bool GATED = false, bool DROP = false>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREADS + (DROP ? 128 : 0), 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREADS + (GATED || DROP ? 128 : 0), 1)
     k_gemm_pair(const __grid_constant__ GemmParams p) {
     static_assert(!GATED || (DQ == DQ_B_K && !SK), "the gated form is a forward on the grid schedule");
     static_assert(!DROP || (DQ == DQ_B_MN && !SK), "the dropout form is a dX GEMM on the grid schedule");
@@ -349,7 +351,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREA
     } else {
         // ------------------------------------------------------------ dequant + epilogue (both CTAs)
         const int ew = warp - 2;
-        const int t = ew * 32 + lane;  // block-row of this CTA's Bop half
+        // GATED: warps 6..9 take no part in the expansion, only in the
+        // epilogue (the second 128 token rows), whose exponentials and
+        // reciprocals would keep four warps busy for twice as long
+        const bool helper = GATED && ew >= S::NDQ_WARPS;
+        const int t = (helper ? 0 : ew) * 32 + lane;  // block-row of this CTA's Bop half
         uint32_t code_off, code_off2, out_off;
         int scale_idx, wrow = 0, kb_off = 0;
         if (DQ == DQ_B_MN) {
@@ -380,7 +386,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREA
         while (sch.next(p, sg)) {
             const int m0 = sg.tm * 512, n0 = sg.tn * 256;
             const int nb0 = n0 + 128 * (int)rank;
-            for (int k = sg.k0; k < sg.k1; ++k, ++it) {
+            for (int k = helper ? sg.k1 : sg.k0; k < sg.k1; ++k, ++it) {
                 const int s = it % STAGES, u = it / STAGES;
                 if (dead) continue;
                 if (!mbar_wait(full_tma(s), u & 1, wc)) {
@@ -420,7 +426,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREA
 
             // -------------------------------------------------------- epilogue of the segment
             if (!dead) {
-                if (mbar_wait(acc_full, seg_i & 1, wc)) {
+                if (helper ? mbar_wait_sleep(acc_full, seg_i & 1, wc, 500) : mbar_wait(acc_full, seg_i & 1, wc)) {
                     tc_fence_after();
                 } else {
                     *abort_flag = 1;
@@ -460,10 +466,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREA
                 }
             }
             // one decision for all four epilogue warps (they meet at named barriers below)
+            constexpr int EPI_THREADS = (S::NDQ_WARPS + (GATED ? 4 : 0)) * 32;
             if (ew == 0 && lane == 0) epi_skip[seg_i & 1] = 0;
-            named_bar(1, S::NDQ_WARPS * 32);
+            named_bar(1, EPI_THREADS);
             if (lane == 0 && (dead || *abort_flag != 0)) epi_skip[seg_i & 1] = 1;
-            named_bar(1, S::NDQ_WARPS * 32);
+            named_bar(1, EPI_THREADS);
             const bool skip = epi_skip[seg_i & 1] != 0;
             const int tid_e = ew * 32 + lane;
             // owner: contributors with a non-empty share, and the prefetch of
@@ -495,11 +502,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREA
             if (GATED && !skip) {
                 // panels of 128 rows x 64 columns: H 0..3, then g 4 + 4 mt + 0..1 and u 4 + 4 mt + 2..3
                 static_assert(12 * 16384 <= S::STAGE_BYTES * STAGES, "the gated epilogue's panels fit the stage buffers");
-                const int act = p.act;
                 const bool keep = p.keep_gu != 0;
+                const int mt = helper ? 1 : 0;
+                auto gate = [&](auto act_tag) {
+                constexpr int act = decltype(act_tag)::value;
 #pragma unroll 1
-                for (int itc = 0; itc < 8; ++itc) {
-                    const int mt = itc >> 2, col0 = (itc & 3) * 32;
+                for (int itc = 0; itc < 4; ++itc) {
+                    const int col0 = itc * 32;
                     uint32_t g[32], u[32];
                     __syncwarp();
                     const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(mt * 256 + col0);
@@ -535,6 +544,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREA
                         }
                     }
                 }
+                };
+                if (p.act == ACT_SILU)
+                    gate(std::integral_constant<int, ACT_SILU>{});
+                else
+                    gate(std::integral_constant<int, ACT_GELU_TANH>{});
             }
             if (!GATED && !skip) {
 #pragma unroll 1
@@ -611,7 +625,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREA
             }
             if (staged) {
                 fence_proxy_async_smem();
-                named_bar(1, S::NDQ_WARPS * 32);
+                named_bar(1, EPI_THREADS);
                 if (GATED && ew == 0 && lane == 0 && !skip) {
 #pragma unroll
                     for (int mt = 0; mt < 2; ++mt)
@@ -647,7 +661,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREA
             // this CTA's accumulators are free for the next segment
             tc_fence_before();
             __syncwarp();
-            if (lane == 0 && !dead) mbar_arrive_cluster(mapa_shared(acc_empty, 0));
+            if (lane == 0 && !dead && !helper) mbar_arrive_cluster(mapa_shared(acc_empty, 0));
             ++seg_i;
         }
     }

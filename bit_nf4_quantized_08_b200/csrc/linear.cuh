@@ -358,7 +358,7 @@ inline cudaError_t launch_gemm_pair(const GemmParams& p, dim3 grid, cudaStream_t
     ProfileScope ps(prof_kind, s);
     note_launch();
     // cluster shape from the kernel's __cluster_dims__
-    return launch_pdl(kern, grid, dim3(PairShape<DQ>::THREADS + (DROP ? 128 : 0), 1, 1), smem, s, 0, p);
+    return launch_pdl(kern, grid, dim3(PairShape<DQ>::THREADS + (GATED || DROP ? 128 : 0), 1, 1), smem, s, 0, p);
 }
 
 // Which large-M GEMM runs: CTA pairs with one pair per tile (default), CTA

@@ -745,12 +745,31 @@ __global__ void k_expand_scales(int64_t rows, int64_t kbs, int dq, const float* 
     // GEMM before) belong to the kernel before it
     pdl_trigger();
     pdl_wait();
-    const int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (idx < nflags) flags[idx] = 0;
-    if (idx >= rows * kbs) return;
-    const int64_t kb = idx / rows, n = idx - kb * rows;
-    const int64_t b = (n * kbs + kb) >> fmt.bs_shift;  // flattened block of the weight's block size
-    scales[kb * ld + n] = dq ? block_scale_dq(q8[b], c1[b >> 8], *offset_ptr, fmt.dq_type) : absmax[b];
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < nflags; i += (int64_t)gridDim.x * blockDim.x)
+        flags[i] = 0;
+    // A 32 x 32 (row, block column) tile through shared memory: the 8-bit
+    // codes are read along a row, the constants written along a block column
+    // (one thread per constant, codes gathered a row apart, took 29 us on
+    // 44032 x 8192; this takes FIXME).
+    __shared__ float tile[32][33];
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;  // 8 warps
+    const int64_t tiles_n = (rows + 31) / 32;
+    const int64_t n0 = (blockIdx.x % tiles_n) * 32, kb0 = (blockIdx.x / tiles_n) * 32;
+    const float off = dq ? *offset_ptr : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t n = n0 + ty + 8 * i, kb = kb0 + tx;
+        if (n < rows && kb < kbs) {
+            const int64_t b = (n * kbs + kb) >> fmt.bs_shift;  // flattened block of the weight's block size
+            tile[ty + 8 * i][tx] = dq ? block_scale_dq(q8[b], c1[b >> 8], off, fmt.dq_type) : absmax[b];
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t kb = kb0 + ty + 8 * i, n = n0 + tx;
+        if (n < rows && kb < kbs) scales[kb * ld + n] = tile[tx][ty + 8 * i];
+    }
 }
 
 __global__ void k_encode(const float* __restrict__ x, int64_t n, uint8_t* __restrict__ codes,
@@ -952,12 +971,12 @@ inline cudaError_t launch_dequantize(const qlora_nf4_weight& w, uint16_t* out, c
 inline cudaError_t launch_expand_scales(const qlora_nf4_weight& w, float* scales, int64_t ld,
                                         cudaStream_t s, int* flags = nullptr, int nflags = 0) {
     const int64_t kbs = w.cols / 64;
-    const int64_t total = w.rows * kbs > nflags ? w.rows * kbs : nflags;
-    if (total == 0) return cudaSuccess;
+    const int64_t tiles = std::max<int64_t>(((w.rows + 31) / 32) * ((kbs + 31) / 32), nflags > 0 ? 1 : 0);
+    if (tiles == 0) return cudaSuccess;
     note_launch();
     // dependent launch: the CTAs can be resident before the kernel ahead
     // ends and wait for it (pdl_wait) before any access
-    return launch_pdl(k_expand_scales, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, s, 0, w.rows, kbs,
+    return launch_pdl(k_expand_scales, dim3((unsigned)tiles), dim3(256), 0, s, 0, w.rows, kbs,
                       (int)w.double_quant, (const float*)w.absmax, (const uint8_t*)w.absmax_q8,
                       (const float*)w.absmax_scale, (const float*)w.absmax_offset, scales, ld, flags, nflags,
                       weight_format(w));
