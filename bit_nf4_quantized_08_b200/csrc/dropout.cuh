@@ -56,12 +56,33 @@ __device__ __forceinline__ uint2 drop_offset(const DropParams& d) {
     return make_uint2((uint32_t)o, (uint32_t)(o >> 32));
 }
 
-// Keep masks of the eight elements of block `blk`: m[j] has 0xFFFF in the low
-// (high) half if element 2j (2j + 1) is kept, else 0.
-__device__ __forceinline__ void drop_mask8(const DropParams& d, uint2 off, uint64_t blk, uint32_t (&m)[4]) {
-    uint32_t c0 = (uint32_t)blk, c1 = (uint32_t)(blk >> 32), c2 = off.x, c3 = off.y;
+// What the first two rounds have in common for all blocks whose number has
+// the same high word (the counter's other words are the launch's): one of the
+// two products of each.  The products are the generator's cost: a 32 x 32 ->
+// 64 bit multiplication issues once in 4 cycles a scheduler, so the 18 that
+// are left take 72 cycles for a warp's 32 blocks (85 measured with all 20).
+struct DropCtx {
+    uint32_t k1, c1, a1, a0;
+};
+__device__ __forceinline__ DropCtx drop_ctx(const DropParams& d, uint2 off, uint32_t blk_hi) {
+    const uint64_t p = (uint64_t)off.x * 0xCD9E8D57u;
+    const uint64_t a = (uint64_t)((uint32_t)(p >> 32) ^ blk_hi ^ d.rk[0]) * 0xD2511F53u;
+    DropCtx c;
+    c.k1 = off.y ^ d.rk[1];
+    c.c1 = (uint32_t)p ^ d.rk[2];
+    c.a1 = (uint32_t)(a >> 32) ^ d.rk[3];
+    c.a0 = (uint32_t)a;
+    return c;
+}
+
+// Keep masks of the eight elements of the block with low word `blk`: m[j] has
+// 0xFFFF in the low (high) half if element 2j (2j + 1) is kept, else 0.
+__device__ __forceinline__ void drop_mask8(const DropParams& d, const DropCtx& x, uint32_t blk, uint32_t (&m)[4]) {
+    const uint64_t p = (uint64_t)blk * 0xD2511F53u;
+    const uint64_t q = (uint64_t)((uint32_t)(p >> 32) ^ x.k1) * 0xCD9E8D57u;
+    uint32_t c0 = (uint32_t)(q >> 32) ^ x.c1, c1 = (uint32_t)q, c2 = (uint32_t)p ^ x.a1, c3 = x.a0;
 #pragma unroll
-    for (int i = 0; i < 10; ++i) {
+    for (int i = 2; i < 10; ++i) {
         const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
         c0 = (uint32_t)(b >> 32) ^ c1 ^ d.rk[2 * i];
         c1 = (uint32_t)b;
@@ -74,14 +95,14 @@ __device__ __forceinline__ void drop_mask8(const DropParams& d, uint2 off, uint6
         m[j] = prmt((w[j] & 0x7FFF7FFFu) + d.add, 0u, 0xBB99u);
 }
 
-// Keep bits of 32 consecutive elements from block `blk`: bit 4 b + j is
-// element 8 b + 2 j, bit 16 + 4 b + j element 8 b + 2 j + 1.
-__device__ __forceinline__ uint32_t drop_bits32(const DropParams& d, uint2 off, uint64_t blk) {
+// Keep bits of 32 consecutive elements from block `blk` (a multiple of 4):
+// bit 4 b + j is element 8 b + 2 j, bit 16 + 4 b + j element 8 b + 2 j + 1.
+__device__ __forceinline__ uint32_t drop_bits32(const DropParams& d, const DropCtx& x, uint32_t blk) {
     uint32_t bits = 0;
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
         uint32_t m[4];
-        drop_mask8(d, off, blk + b, m);
+        drop_mask8(d, x, blk + b, m);
 #pragma unroll
         for (int j = 0; j < 4; ++j) bits |= m[j] & (0x00010001u << (4 * b + j));
     }
@@ -95,65 +116,58 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 // Y[e] = kept(e) ? X[e] * up : +0, elementwise (X and Y may be the same).
 // A dropped element gives +0 whatever X holds there.  bf16 products are
 // formed in fp32 and rounded once.
-// Bound by HBM: each element is read and written once.  A thread takes whole
-// eight-element blocks (16 bytes of bf16, 32 of fp32), UNROLL of them one
-// grid stride apart with all their loads issued first.
+// Bound by HBM: each element is read and written once (2^27 bf16: 90 us, 5.96
+// TB/s; the generator alone would take about 38 us).  A thread takes whole
+// eight-element blocks: 16 bytes of bf16, 32 of fp32.
 // ---------------------------------------------------------------------------
-template <typename T, int UNROLL>
-__global__ void __launch_bounds__(256) k_dropout(const T* X, T* Y, int64_t n, const __grid_constant__ DropParams d) {
+template <typename T>
+__global__ void __launch_bounds__(256, 8) k_dropout(const T* X, T* Y, int64_t n, const __grid_constant__ DropParams d) {
     constexpr bool F32 = sizeof(T) == 4;
     pdl_trigger();
     pdl_wait();
     const uint2 off = drop_offset(d);
+    uint32_t hi = 0;
+    DropCtx ctx = drop_ctx(d, off, 0u);
+    auto mask = [&](int64_t b, uint32_t (&m)[4]) {
+        if ((uint32_t)(b >> 32) != hi) {  // past 2^35 elements
+            hi = (uint32_t)(b >> 32);
+            ctx = drop_ctx(d, off, hi);
+        }
+        drop_mask8(d, ctx, (uint32_t)b, m);
+    };
     const int64_t full = n >> 3;
     const int64_t stride = (int64_t)gridDim.x * blockDim.x;
     const int64_t t0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     const uint4* xv = reinterpret_cast<const uint4*>(X);
     uint4* yv = reinterpret_cast<uint4*>(Y);
-    for (int64_t b0 = t0; b0 < full; b0 += stride * UNROLL) {
-        uint4 v[UNROLL][F32 ? 2 : 1];
+    for (int64_t b = t0; b < full; b += stride) {
+        uint32_t m[4] = {~0u, ~0u, ~0u, ~0u};
+        if (F32) {
+            const uint4 v0 = xv[2 * b], v1 = xv[2 * b + 1];
+            if (d.thr) mask(b, m);
+            uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
-        for (int q = 0; q < UNROLL; ++q) {
-            const int64_t b = b0 + q * stride;
-            if (b < full) {
-                if (F32) {
-                    v[q][0] = xv[2 * b];
-                    v[q][F32 ? 1 : 0] = xv[2 * b + 1];
-                } else {
-                    v[q][0] = xv[b];
-                }
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t keep = (i & 1) ? prmt(m[i >> 1], 0u, 0x3232u) : prmt(m[i >> 1], 0u, 0x1010u);
+                w[i] = __float_as_uint(__fmul_rn(__uint_as_float(w[i]), d.up)) & keep;
             }
-        }
+            yv[2 * b] = make_uint4(w[0], w[1], w[2], w[3]);
+            yv[2 * b + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+        } else {
+            const uint4 v = xv[b];
+            if (d.thr) mask(b, m);
+            uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int q = 0; q < UNROLL; ++q) {
-            const int64_t b = b0 + q * stride;
-            if (b >= full) break;
-            uint32_t m[4] = {~0u, ~0u, ~0u, ~0u};
-            if (d.thr) drop_mask8(d, off, (uint64_t)b, m);
-            if (F32) {
-                uint32_t w[8] = {v[q][0].x, v[q][0].y, v[q][0].z, v[q][0].w,
-                                 v[q][F32 ? 1 : 0].x, v[q][F32 ? 1 : 0].y, v[q][F32 ? 1 : 0].z, v[q][F32 ? 1 : 0].w};
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t keep = (i & 1) ? prmt(m[i >> 1], 0u, 0x3232u) : prmt(m[i >> 1], 0u, 0x1010u);
-                    w[i] = __float_as_uint(__fmul_rn(__uint_as_float(w[i]), d.up)) & keep;
-                }
-                yv[2 * b] = make_uint4(w[0], w[1], w[2], w[3]);
-                yv[2 * b + 1] = make_uint4(w[4], w[5], w[6], w[7]);
-            } else {
-                uint32_t w[4] = {v[q][0].x, v[q][0].y, v[q][0].z, v[q][0].w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    w[j] = pack_bf16x2(__fmul_rn(bf16_lo(w[j]), d.up), __fmul_rn(bf16_hi(w[j]), d.up)) & m[j];
-                yv[b] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            for (int j = 0; j < 4; ++j)
+                w[j] = pack_bf16x2(__fmul_rn(bf16_lo(w[j]), d.up), __fmul_rn(bf16_hi(w[j]), d.up)) & m[j];
+            yv[b] = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
     // the last, partial block
     const int tail = (int)(n & 7);
     if (tail && t0 == 0) {
         uint32_t m[4] = {~0u, ~0u, ~0u, ~0u};
-        if (d.thr) drop_mask8(d, off, (uint64_t)full, m);
+        if (d.thr) mask(full, m);
         for (int i = 0; i < tail; ++i) {
             const int64_t e = 8 * full + i;
             const bool keep = (m[i >> 1] >> (16 * (i & 1))) & 1u;

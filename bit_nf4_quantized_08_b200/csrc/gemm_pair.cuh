@@ -325,8 +325,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREA
         for (int mt = 0; mt < 2; ++mt) {
             const int64_t m = sg.tm * 512 + 256 * mt + 128 * (int)rank + quarter * 32 + lane;
             const uint64_t blk = (uint64_t)((m * p.cols + sg.tn * 256) >> 3);
+            uint32_t hi = (uint32_t)(blk >> 32);
+            DropCtx ctx = drop_ctx(p.dp, off, hi);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) keep[mt * 8 + c] = drop_bits32(p.dp, off, blk + 4 * c);
+            for (int c = 0; c < 8; ++c) {
+                if ((uint32_t)((blk + 4 * c) >> 32) != hi) {  // (blk is a multiple of 8: no four blocks straddle)
+                    hi = (uint32_t)((blk + 4 * c) >> 32);
+                    ctx = drop_ctx(p.dp, off, hi);
+                }
+                keep[mt * 8 + c] = drop_bits32(p.dp, ctx, (uint32_t)blk + 4 * c);
+            }
         }
         if (__all_sync(0xffffffffu, mbar_wait(lora_full, 0, wc))) {
             tc_fence_after();

@@ -125,8 +125,8 @@ inline int skinny_active_clusters(int cs) {
 
 template <int BN, bool DROP>
 inline cudaError_t launch_skinny(SkinnyParams& p, int tiles, int kmin, int kmax, cudaStream_t s) {
-    constexpr int threads = SkinnyShape<BN>::THREADS + (DROP ? 32 * (kMaskWarps - 4) : 0);
-    constexpr int smem = SkinnyShape<BN>::SMEM;
+    constexpr int threads = SkinnyShape<BN, DROP>::THREADS;
+    constexpr int smem = SkinnyShape<BN, DROP>::SMEM;
     static_assert(smem <= 232448, "shared memory per CTA");
     // Cluster size: fewest rounds of resident clusters times k-steps per CTA
     // (plus a fixed per-CTA cost of about three k-steps), at least one
@@ -161,12 +161,12 @@ inline cudaError_t launch_skinny(SkinnyParams& p, int tiles, int kmin, int kmax,
 
 template <int BN, bool DROP>
 inline cudaError_t launch_lora_stream(SkinnyParams& p, int tiles, int nctas, cudaStream_t s) {
-    constexpr int smem = StreamShape<BN>::SMEM;
+    constexpr int smem = StreamShape<BN, DROP>::SMEM;
     static_assert(smem <= 232448, "shared memory per CTA");
     for (int i = 0; i < p.nprob; ++i) p.pr[i].per = p.pr[i].ksteps;
     p.total_tiles = tiles;
     p.pack = 0;
-    constexpr int threads = StreamShape<BN>::THREADS + (DROP ? 32 * kMaskWarps : 0);
+    constexpr int threads = StreamShape<BN, DROP>::THREADS;
     auto kern = k_lora_stream<BN, DROP>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -871,16 +871,19 @@ inline unsigned elementwise_grid(int64_t n) {
     return (unsigned)std::max<int64_t>(1, std::min<int64_t>((n + 255) / 256, (int64_t)sm_count() * 8));
 }
 
-// Y = dropout(X), n elements: four blocks of eight in flight a thread for
-// bf16 (64 bytes), two for fp32 (64 bytes).
+// Y = dropout(X), n elements: one block of eight a thread and pass, eight CTAs
+// an SM (32 registers; with more blocks in flight a thread the generators
+// interleave, take 64 to 98 registers and leave too few warps: 107 to 127 us
+// on 2^27 bf16 instead of 90 us), and 64 CTAs an SM (94 us with 16; 115 us
+// with one pass a CTA, whose launches then cost more than the loop).
 inline cudaError_t launch_dropout(const void* X, bool is_bf16, int64_t n, const DropParams& d, void* Y,
                                   cudaStream_t s) {
     note_launch();
-    const unsigned grid = elementwise_grid(n / 8 + 1);
+    const unsigned grid = (unsigned)std::min<int64_t>((n / 8 + 256) / 256, (int64_t)sm_count() * 64);
     if (is_bf16)
-        return launch_pdl(k_dropout<uint16_t, 4>, dim3(grid), dim3(256), 0, s, 0, static_cast<const uint16_t*>(X),
+        return launch_pdl(k_dropout<uint16_t>, dim3(grid), dim3(256), 0, s, 0, static_cast<const uint16_t*>(X),
                           static_cast<uint16_t*>(Y), n, d);
-    return launch_pdl(k_dropout<float, 2>, dim3(grid), dim3(256), 0, s, 0, static_cast<const float*>(X),
+    return launch_pdl(k_dropout<float>, dim3(grid), dim3(256), 0, s, 0, static_cast<const float*>(X),
                       static_cast<float*>(Y), n, d);
 }
 

@@ -86,37 +86,43 @@ struct SkinnyParams {
 // Adapter dropout: the A tiles of X pass through mask warps between their TMA
 // load and the MMA.  A tile is 128 lines of 64 consecutive elements of X
 // (K-major: a token row each; MN-major: 64 tokens of each of two 64-column
-// chunks), eight generator blocks a line.  Thread t of the 256 takes half of
-// line t % 128: its four blocks' masks, each ANDed onto one 16-byte chunk of
+// chunks), eight generator blocks a line.  Three or four groups of four warps take the
+// k-steps in turn (the ring is a whole number of turns, so that a group always
+// meets the same stages and its phase parities follow on), thread t of a group line t: its eight masks are generated
+// before the tile is waited for, then each is ANDed onto one 16-byte chunk of
 // the 128-byte-swizzled line (eight neighbouring lines give eight different
-// chunks, so the accesses are free of bank conflicts).  The generator, about
-// 55 instructions a block, sets the pace: with eight warps about 300 cycles a
-// tile, near the time a tile takes to arrive.
-constexpr int kMaskWarps = 8;
+// chunks, so the accesses are free of bank conflicts).  What bounds one group
+// is the latency from the landed tile to the MMA's barrier (accesses, proxy
+// fence, arrival), about 0.8 us however many warps share a tile; with several
+// k-steps on the way at once the generator sets the pace (32 warp-wide blocks
+// a tile, 610 cycles over the four schedulers at its multiplication rate).
+constexpr int mask_groups(int stages) { return stages % 4 == 0 ? 4 : stages; }
 
-// Element index of the first element of line l of the A tile of rows m0.. at k-step k.
-__device__ __forceinline__ int64_t drop_line(const SkinnyProblem& P, int64_t cols, int m0, int k, int l) {
-    return P.a_mn ? (int64_t)(k * 64 + (l & 63)) * cols + m0 + (l & ~63)
-                  : (int64_t)(m0 + l) * cols + (int64_t)k * 64;
+struct DropTile {
+    uint32_t m[8][4];
+};
+
+// Masks of line l of the A tile of rows m0.. at k-step k.
+__device__ __forceinline__ void drop_generate(DropTile& o, const SkinnyProblem& P, const DropParams& d, uint2 off,
+                                              int64_t cols, int m0, int k, int l) {
+    const int64_t e = P.a_mn ? (int64_t)(k * 64 + (l & 63)) * cols + m0 + (l & ~63)
+                             : (int64_t)(m0 + l) * cols + (int64_t)k * 64;
+    const uint64_t blk = (uint64_t)(e >> 3);  // a multiple of 8: the line's blocks share the high word
+    const DropCtx x = drop_ctx(d, off, (uint32_t)(blk >> 32));
+#pragma unroll
+    for (int q = 0; q < 8; ++q) drop_mask8(d, x, (uint32_t)blk + q, o.m[q]);
 }
-
-// Masks the tile at shared address sA (t: 0..255).
-__device__ __forceinline__ void drop_tile(const SkinnyProblem& P, const DropParams& d, uint2 off, int64_t cols, int m0,
-                                          int k, uint32_t sA, int t) {
-    const int l = t & 127, q0 = (t >> 7) * 4;
-    const uint64_t blk = (uint64_t)(drop_line(P, cols, m0, k, l) >> 3) + q0;
-    uint32_t m[4][4];
+// Applies them to the tile at shared address sA.
+__device__ __forceinline__ void drop_apply(const DropTile& o, uint32_t sA, int l) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) drop_mask8(d, off, blk + q, m[q]);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const uint32_t a = sA + (uint32_t)l * 128u + (uint32_t)(((q0 + q) ^ (l & 7)) << 4);
+    for (int q = 0; q < 8; ++q) {
+        const uint32_t a = sA + (uint32_t)l * 128u + (uint32_t)((q ^ (l & 7)) << 4);
         const uint4 v = ld_shared_v4(a);
-        st_shared_v4(a, v.x & m[q][0], v.y & m[q][1], v.z & m[q][2], v.w & m[q][3]);
+        st_shared_v4(a, v.x & o.m[q][0], v.y & o.m[q][1], v.z & o.m[q][2], v.w & o.m[q][3]);
     }
 }
 
-template <int BN>
+template <int BN, bool DROP = false>
 struct SkinnyShape {
     static constexpr int A_BYTES = 128 * 128;
     static constexpr int B_BYTES = BN * 128;
@@ -125,13 +131,15 @@ struct SkinnyShape {
     // reduction buffer [cs][128 / cs][PART_LD] (cs a power of two <= 8)
     static constexpr int RED_BYTES = 128 * PART_LD * 4;
     static constexpr bool RED_OVERLAY = BN > 128;
-    static constexpr int STAGES = BN <= 64 ? 7 : (BN <= 128 ? 4 : 3);
+    static constexpr int STAGES = BN <= 64 ? (DROP ? 6 : 7) : (BN <= 128 ? 4 : 3);
+    static constexpr int GROUPS = mask_groups(STAGES);  // DROP: of four mask warps
+    static_assert(!DROP || STAGES % GROUPS == 0, "the ring is a whole number of turns");
     static constexpr int PIPE_BYTES = STAGE_BYTES * STAGES;
     static constexpr int RED_OFF = RED_OVERLAY ? 0 : PIPE_BYTES;
     static constexpr int REGION = RED_OVERLAY ? (PIPE_BYTES > RED_BYTES ? PIPE_BYTES : RED_BYTES)
                                               : PIPE_BYTES + RED_BYTES;
     static constexpr int SMEM = REGION + 1024 + 256;
-    static constexpr int THREADS = 32 * 6;  // producer, MMA, 4 epilogue warps
+    static constexpr int THREADS = 32 * (2 + 4 * (DROP ? GROUPS : 1));  // producer, MMA, 4 epilogue warps (the first mask group)
 };
 
 __device__ __forceinline__ void cluster_arrive() {
@@ -154,9 +162,8 @@ __device__ __forceinline__ void st_async_v4(uint32_t addr, uint32_t a, uint32_t 
 }
 
 template <int BN, bool DROP = false>
-__global__ void __launch_bounds__(SkinnyShape<BN>::THREADS + (DROP ? 32 * (kMaskWarps - 4) : 0), 1)
-    k_skinny(const __grid_constant__ SkinnyParams p) {
-    using S = SkinnyShape<BN>;
+__global__ void __launch_bounds__(SkinnyShape<BN, DROP>::THREADS, 1) k_skinny(const __grid_constant__ SkinnyParams p) {
+    using S = SkinnyShape<BN, DROP>;
     constexpr int STAGES = S::STAGES;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_base = smem_u32(smem_raw);
@@ -197,7 +204,7 @@ __global__ void __launch_bounds__(SkinnyShape<BN>::THREADS + (DROP ? 32 * (kMask
             mbar_init(empty(s), 1);
         }
         if (DROP)
-            for (int s = 0; s < STAGES; ++s) mbar_init(masked(s), kMaskWarps);
+            for (int s = 0; s < STAGES; ++s) mbar_init(masked(s), 4);  // one group's warps
         mbar_init(acc_full, 1);
         mbar_init(red_full, 1);
         // every rank (this one included) sends rows_per rows of rc floats here
@@ -260,21 +267,25 @@ __global__ void __launch_bounds__(SkinnyShape<BN>::THREADS + (DROP ? 32 * (kMask
         if (lane == 0) {
             const uint32_t idesc = idesc_bf16_f32(128, BN, a_mn, b_mn);
             const bool drop = DROP && P.drop;
+            // stage, phase and descriptors advance by additions: this thread
+            // shares its scheduler with busy mask warps
+            const uint64_t ad0 = smem_desc_sw128(base, a_mn ? 8192 : 16, 1024);
+            const uint64_t bd0 = smem_desc_sw128(base + S::A_BYTES, b_mn ? 8192 : 16, 1024);
+            const uint32_t astep = a_mn ? 2048 >> 4 : 32 >> 4, bstep = b_mn ? 2048 >> 4 : 32 >> 4;
+            const uint32_t ready = drop ? masked(0) : full(0);
+            uint32_t s = 0, ph = 0;
             for (int i = 0; i < nk; ++i) {
-                const int s = i % STAGES, u = i / STAGES;
-                if (!mbar_wait(drop ? masked(s) : full(s), u & 1, wc)) { *abort_flag = 1; break; }
+                if (!mbar_wait(ready + 8u * s, ph, wc)) { *abort_flag = 1; break; }
                 tc_fence_after();
-                const uint32_t sA = base + s * S::STAGE_BYTES;
-                const uint32_t sB = sA + S::A_BYTES;
+                const uint64_t so = (uint64_t)(s * (uint32_t)(S::STAGE_BYTES >> 4));
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    const uint64_t ad = a_mn ? smem_desc_sw128(sA + kk * 2048, 8192, 1024)
-                                             : smem_desc_sw128(sA + kk * 32, 16, 1024);
-                    const uint64_t bd = b_mn ? smem_desc_sw128(sB + kk * 2048, 8192, 1024)
-                                             : smem_desc_sw128(sB + kk * 32, 16, 1024);
-                    umma_bf16(tmem, ad, bd, idesc, (i > 0 || kk > 0) ? 1u : 0u);
+                for (uint32_t kk = 0; kk < 4; ++kk)
+                    umma_bf16(tmem, ad0 + so + kk * astep, bd0 + so + kk * bstep, idesc, (i > 0 || kk > 0) ? 1u : 0u);
+                umma_commit(empty((int)s));
+                if (++s == (uint32_t)STAGES) {
+                    s = 0;
+                    ph ^= 1u;
                 }
-                umma_commit(empty(s));
             }
             umma_commit(acc_full);
             // the MMAs (and their reads of shared memory) are complete before
@@ -284,13 +295,16 @@ __global__ void __launch_bounds__(SkinnyShape<BN>::THREADS + (DROP ? 32 * (kMask
     }
 
     if (DROP && warp >= 2 && P.drop) {
-        // ------------------------------------------------------------ mask warps (the epilogue's and four more)
+        // ------------------------------------------------------------ mask warps (the epilogue's four the first group)
         if (p.wait_first) pdl_wait();  // the offset's device counter
         const uint2 off = drop_offset(p.dp);
-        for (int i = 0; i < nk; ++i) {
+        const int line = ((warp - 2) & 3) * 32 + lane;
+        for (int i = (warp - 2) >> 2; i < nk; i += S::GROUPS) {
             const int s = i % STAGES, u = i / STAGES;
+            DropTile dt;
+            drop_generate(dt, P, p.dp, off, p.drop_cols, m0, k0 + i, line);
             if (!__all_sync(0xffffffffu, mbar_wait(full(s), u & 1, wc))) { *abort_flag = 1; break; }
-            drop_tile(P, p.dp, off, p.drop_cols, m0, k0 + i, base + s * S::STAGE_BYTES, (int)threadIdx.x - 64);
+            drop_apply(dt, base + s * S::STAGE_BYTES, line);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(masked(s));
@@ -414,7 +428,7 @@ __global__ void __launch_bounds__(SkinnyShape<BN>::THREADS + (DROP ? 32 * (kMask
 // tile's loads and MMAs.  Same operands, layouts and output modes as
 // k_skinny; per tile the result equals k_skinny's with a cluster of 1.
 // ---------------------------------------------------------------------------
-template <int BN>
+template <int BN, bool DROP = false>
 struct StreamShape {
     static constexpr int A_BYTES = 128 * 128;
     static constexpr int B_BYTES = BN * 128;
@@ -426,14 +440,16 @@ struct StreamShape {
     static_assert(STAGES % CG == 0, "the ring holds whole commit groups");
     static constexpr int PIPE_BYTES = STAGE_BYTES * STAGES;
     static constexpr int SMEM = PIPE_BYTES + 1024 + 512;
-    static constexpr int THREADS = 32 * 6;  // producer, MMA, 4 epilogue warps
+    static constexpr int GROUPS = mask_groups(STAGES);  // DROP: of four mask warps
+    static_assert(STAGES % GROUPS == 0, "the ring is a whole number of turns");
+    static constexpr int THREADS = 32 * (6 + (DROP ? 4 * GROUPS : 0));  // producer, MMA, 4 epilogue warps, mask warps
     static constexpr int TMEM_COLS = 2 * BN;
 };
 
 template <int BN, bool DROP = false>
-__global__ void __launch_bounds__(StreamShape<BN>::THREADS + (DROP ? 32 * kMaskWarps : 0), 1)
+__global__ void __launch_bounds__(StreamShape<BN, DROP>::THREADS, 1)
     k_lora_stream(const __grid_constant__ SkinnyParams p) {
-    using S = StreamShape<BN>;
+    using S = StreamShape<BN, DROP>;
     constexpr int STAGES = S::STAGES;
     constexpr int RING = 4;  // tile indices handed from the producer to the MMA and epilogue warps
     extern __shared__ uint8_t smem_raw[];
@@ -488,10 +504,10 @@ __global__ void __launch_bounds__(StreamShape<BN>::THREADS + (DROP ? 32 * kMaskW
         }
         for (int j = 0; j < RING; ++j) {
             mbar_init(tile_full(j), 1);
-            mbar_init(tile_empty(j), 5 + (DROP ? kMaskWarps : 0));  // MMA thread, 4 epilogue warps, mask warps
+            mbar_init(tile_empty(j), 5 + (DROP ? 4 * S::GROUPS : 0));  // MMA thread, 4 epilogue warps, mask warps
         }
         if (DROP)
-            for (int s = 0; s < STAGES; ++s) mbar_init(masked(s), kMaskWarps);
+            for (int s = 0; s < STAGES; ++s) mbar_init(masked(s), 4);  // one group's warps
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -631,6 +647,7 @@ __global__ void __launch_bounds__(StreamShape<BN>::THREADS + (DROP ? 32 * kMaskW
         // (whatever wrote the offset's device counter completed before the
         // kernel ahead let this one start)
         const uint2 off = drop_offset(p.dp);
+        const int group = (warp - 6) >> 2, line = ((warp - 6) & 3) * 32 + lane;
         bool ok = true;
         int it = 0;
         for (int li = 0; ok; ++li) {
@@ -642,15 +659,17 @@ __global__ void __launch_bounds__(StreamShape<BN>::THREADS + (DROP ? 32 * kMaskW
             locate(t, pi, tile);
             const SkinnyProblem& P = p.pr[pi];
             for (int k = 0; k < P.ksteps; ++k, ++it) {
+                if (it % S::GROUPS != group) continue;
                 const int s = it % STAGES;
+                DropTile dt;
+                if (P.drop) drop_generate(dt, P, p.dp, off, p.drop_cols, tile * 128, k, line);
                 if (!__all_sync(0xffffffffu, mbar_wait(full(s), (it / STAGES) & 1, wc))) {
                     *abort_flag = 1;
                     ok = false;
                     break;
                 }
                 if (P.drop) {
-                    drop_tile(P, p.dp, off, p.drop_cols, tile * 128, k, base + s * S::STAGE_BYTES,
-                              (int)threadIdx.x - 32 * 6);
+                    drop_apply(dt, base + s * S::STAGE_BYTES, line);
                     fence_proxy_async_smem();
                 }
                 __syncwarp();
