@@ -37,12 +37,18 @@ struct PairShape {
     static constexpr int STAGE_BYTES = (STAGE_RAW + 1023) / 1024 * 1024;
     static constexpr int NDQ_WARPS = 4;
     static constexpr int THREADS = 32 * (2 + NDQ_WARPS);
+    static constexpr int NMASK_WARPS = 8;            // dropout form
+    static constexpr int KEEP_BYTES = 8 * 256 * 4;   // dropout form: the keep bits of a CTA's 256 x 256 half tile
+    template <bool GATED, bool DROP>
+    static constexpr int threads() {
+        return THREADS + (GATED ? 128 : 0) + (DROP ? 32 * NMASK_WARPS : 0);
+    }
     static constexpr int TMEM_COLS = 512;
 };
 
-template <int DQ, int STAGES>
+template <int DQ, int STAGES, bool DROP = false>
 constexpr int pair_smem_bytes() {
-    return PairShape<DQ>::STAGE_BYTES * STAGES + 1024 + 256;
+    return PairShape<DQ>::STAGE_BYTES * STAGES + 1024 + 256 + (DROP ? PairShape<DQ>::KEEP_BYTES : 0);
 }
 
 // Physical offset inside a TMA tile written with the 64-byte swizzle.
@@ -117,13 +123,13 @@ struct PairSchedule {
 //
 // DROP (dX under adapter dropout): the adapter's term sG A is masked, the base
 // term is not, and both sums share an accumulator (the two accumulators fill
-// TMEM).  So the LoRA k-steps run first; four more warps mask their sum in
+// TMEM).  So the LoRA k-steps run first; eight more warps mask their sum in
 // TMEM (load, select by the recomputed keep bits, store), and the main k-steps
 // accumulate onto it: one rounding, no traffic besides sG and A.  The keep
-// bits of a thread's 512 elements (16 registers) are generated while the first
-// operands are on their way.
+// bits are generated while the first operands are on their way (256 warp-wide
+// generator blocks a CTA, 3 us).
 template <int DQ, int STAGES, bool SK, bool GATED = false, bool DROP = false>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREADS + (GATED || DROP ? 128 : 0), 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::template threads<GATED, DROP>(), 1)
     k_gemm_pair(const __grid_constant__ GemmParams p) {
     static_assert(!GATED || (DQ == DQ_B_K && !SK), "the gated form is a forward on the grid schedule");
     static_assert(!DROP || (DQ == DQ_B_MN && !SK), "the dropout form is a dX GEMM on the grid schedule");
@@ -167,7 +173,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREA
         for (int j = 0; j < PF_SLOTS; ++j) mbar_init(pf_full(j), 1);
         if (DROP) {
             mbar_init(lora_full, 1);
-            mbar_init(lora_done, 2 * S::NDQ_WARPS);
+            mbar_init(lora_done, 2 * S::NMASK_WARPS);
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -313,40 +319,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<DQ>::THREA
         }
     } else if (DROP && warp >= 2 + S::NDQ_WARPS) {
         // ------------------------------------------------------------ mask warps (both CTAs)
-        const int quarter = warp & 3;
+        // warps 6..9 take the first 128 token rows, 10..13 the second; both
+        // loops stay rolled (unrolled, their 60 KB of straight-line code cost
+        // more in instruction fetches, about 15 us a tile, than the work)
+        const int quarter = warp & 3, mt = (warp - 2 - S::NDQ_WARPS) >> 2;
         PairSchedule<SK> sch(p);
         PairSeg sg;
         sch.next(p, sg);
         // (whatever wrote the offset's device counter completed before the
         // kernel ahead let this one start)
         const uint2 off = drop_offset(p.dp);
-        uint32_t keep[16];
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-            const int64_t m = sg.tm * 512 + 256 * mt + 128 * (int)rank + quarter * 32 + lane;
-            const uint64_t blk = (uint64_t)((m * p.cols + sg.tn * 256) >> 3);
-            uint32_t hi = (uint32_t)(blk >> 32);
-            DropCtx ctx = drop_ctx(p.dp, off, hi);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                if ((uint32_t)((blk + 4 * c) >> 32) != hi) {  // (blk is a multiple of 8: no four blocks straddle)
-                    hi = (uint32_t)((blk + 4 * c) >> 32);
-                    ctx = drop_ctx(p.dp, off, hi);
-                }
-                keep[mt * 8 + c] = drop_bits32(p.dp, ctx, (uint32_t)blk + 4 * c);
+        const int64_t m = sg.tm * 512 + 256 * mt + 128 * (int)rank + quarter * 32 + lane;
+        const uint64_t blk0 = (uint64_t)((m * p.cols + sg.tn * 256) >> 3);
+        uint32_t hi = (uint32_t)(blk0 >> 32);
+        DropCtx ctx = drop_ctx(p.dp, off, hi);
+        // this thread's keep words (32 columns each), one per 4 KB plane
+        uint32_t* keep = reinterpret_cast<uint32_t*>(gbase + S::STAGE_BYTES * STAGES + 256) + (warp - 6) * 32 + lane;
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+            const uint64_t blk = blk0 + 4 * c;
+            if ((uint32_t)(blk >> 32) != hi) {  // (blk0 is a multiple of 8: no four blocks straddle)
+                hi = (uint32_t)(blk >> 32);
+                ctx = drop_ctx(p.dp, off, hi);
             }
+            keep[c * 256] = drop_bits32(p.dp, ctx, (uint32_t)blk);
         }
         if (__all_sync(0xffffffffu, mbar_wait(lora_full, 0, wc))) {
             tc_fence_after();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(i * 32);
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+                const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(mt * 256 + c * 32);
+                const uint32_t kw = keep[c * 256];
                 uint32_t v[32];
                 tmem_ld_32x32b_x32(ta, v);
                 tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
-                    if (!(keep[i] & (1u << ((e >> 1) + 16 * (e & 1))))) v[e] = 0u;
+                    if (!(kw & (1u << ((e >> 1) + 16 * (e & 1))))) v[e] = 0u;
                 tmem_st_32x32b_x32(ta, v);
             }
             tmem_st_wait();

@@ -348,7 +348,7 @@ inline size_t linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int r, int
 // per tile.  Debug mode 2 forces stream-K on 7 CTAs (tests of the merge).
 template <int DQ, int STAGES, bool GATED = false, bool DROP = false>
 inline cudaError_t launch_gemm_pair(const GemmParams& p, dim3 grid, cudaStream_t s, int prof_kind) {
-    constexpr int smem = pair_smem_bytes<DQ, STAGES>();
+    constexpr int smem = pair_smem_bytes<DQ, STAGES, DROP>();
     static_assert(smem <= 232448, "shared memory per CTA");
     auto kern = GATED || DROP ? k_gemm_pair<DQ, STAGES, false, GATED, DROP>
                 : p.streamk   ? k_gemm_pair<DQ, STAGES, true>
@@ -358,7 +358,7 @@ inline cudaError_t launch_gemm_pair(const GemmParams& p, dim3 grid, cudaStream_t
     ProfileScope ps(prof_kind, s);
     note_launch();
     // cluster shape from the kernel's __cluster_dims__
-    return launch_pdl(kern, grid, dim3(PairShape<DQ>::THREADS + (GATED || DROP ? 128 : 0), 1, 1), smem, s, 0, p);
+    return launch_pdl(kern, grid, dim3(PairShape<DQ>::template threads<GATED, DROP>(), 1, 1), smem, s, 0, p);
 }
 
 // Which large-M GEMM runs: CTA pairs with one pair per tile (default), CTA
