@@ -59,7 +59,7 @@ cudaError_t launch_encode(const float* x, int64_t n, uint8_t* codes, cudaStream_
 // Block constants a' of a weight, written transposed as scales[kb * ld + n]
 // (kb = block column, n = row) for the GEMM producers.
 cudaError_t launch_expand_scales(const qlora_nf4_weight& w, float* scales, int64_t ld,
-                                 cudaStream_t s, int* flags, int nflags);
+                                 cudaStream_t s, int* flags, int nflags, int beside);
 
 // ---- GEMMs (gemm.cu) ----
 // r is the rank of each adapter.  A fused projection (nseg > 1) is one
@@ -77,6 +77,10 @@ struct LinearArgs {
     // kept elements
     const struct DropParams* drop;
     int grad_bf16;  // dA and dB in bf16 instead of fp32
+    // gated backward: dY's kernel has formed sG too, in split partial sums
+    // (sG_part) or, unsplit, in the workspace
+    int have_sG;
+    const float* sG_part;
     int rt() const { return r * nseg; }  // columns of sU and sG
 };
 qlora_status linear_fwd_impl(const void* X, const LinearArgs& a, const void* A, const void* B,

