@@ -55,25 +55,6 @@ __device__ __forceinline__ void act_value_grad(int act, float g, float* v, float
     *dv = s + x * (2.0f * 0.7978845608028654f) * (1.0f + 0.134145f * g2) * s * (1.0f - s);
 }
 
-// H[m][f] = act(GU[m][f]) GU[m][F + f]; eight columns a thread.
-__global__ void __launch_bounds__(256) k_gated_act(const uint16_t* GU, uint16_t* H, int64_t M, int64_t F, int act) {
-    pdl_trigger();
-    pdl_wait();
-    const int64_t f8 = F / 8;
-    for (int64_t b = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; b < M * f8;
-         b += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t m = b / f8, c = b - m * f8;
-        const uint4 gv = *reinterpret_cast<const uint4*>(GU + m * 2 * F + c * 8);
-        const uint4 uv = *reinterpret_cast<const uint4*>(GU + m * 2 * F + F + c * 8);
-        const uint32_t g[4] = {gv.x, gv.y, gv.z, gv.w}, u[4] = {uv.x, uv.y, uv.z, uv.w};
-        uint32_t o[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            o[q] = pack_bf16x2(act_value(act, bf16_lo(g[q])) * bf16_lo(u[q]), act_value(act, bf16_hi(g[q])) * bf16_hi(u[q]));
-        *reinterpret_cast<uint4*>(H + m * F + c * 8) = make_uint4(o[0], o[1], o[2], o[3]);
-    }
-}
-
 // Eight columns of [dG | dU] from dH, g and u.
 template <int act>
 __device__ __forceinline__ void gated_grad8(const uint4& hv, const uint4& gv, const uint4& uv, uint32_t (&og)[4],

@@ -22,6 +22,7 @@
 
 #include "dropout.cuh"
 #include "gated.cuh"
+#include "gated_small.cuh"
 #include "gemm.cuh"
 #include "gemm_pair.cuh"
 #include "skinny.cuh"
@@ -708,7 +709,7 @@ inline qlora_status linear_fwd_impl(const void* X, const LinearArgs& a, const vo
     return launch_small_m(X, a, B, Y, L, s);
 }
 
-// H = act(g) u for M > 64 on the gated form of the pair kernel, one pair per
+// H = act(g) u for M > kGatedSmall on the gated form of the pair kernel, one pair per
 // tile of 512 tokens x 128 hidden columns whatever schedule the linears use.
 inline qlora_status gated_fwd_large(const void* X, const LinearArgs& a, const void* A, const void* B, int act, void* H,
                                     void* GU, void* ws, cudaStream_t s) {
@@ -1028,46 +1029,114 @@ inline qlora_status linear_bwd_impl(const void* dY, const void* X, const LinearA
 }
 
 // ---------------------------------------------------------------------------
-// Adapter dropout and the gated feed-forward on the linear's forward and
-// backward.  Workspace: the linear's, then the pre-activations [M, 2F] that
-// the caller does not keep (gated forward, few tokens) or their gradient
-// (gated backward).
+// The gated feed-forward.  Workspace: backward and forward of more than
+// kGatedSmall tokens, the linear's; backward, then the gradient of the
+// pre-activations [M, 2F] and the split partial sums of sG; forward of few
+// tokens, sU, the partial tiles and their arrival counters.
 // ---------------------------------------------------------------------------
+constexpr int kGatedSmall = 128;
+
 struct BlockWs {
     void* linear;
     size_t linear_bytes;
     uint16_t* gu;
-    float* grad_part;  // gated backward with adapters: split partial sums of sG
+    float* grad_part;
+    uint16_t* sU;
+    float* part;
+    size_t part_floats;
+    unsigned long long* counters;
     size_t bytes;
 };
 
-inline BlockWs carve_block_ws(void* ws, int64_t M, int64_t N, int64_t K, int rt, int bwd, int gated) {
+inline BlockWs carve_block_ws(void* ws, int64_t M, int64_t N, int64_t K, int rt, int bwd) {
     BlockWs b;
-    b.linear_bytes = linear_workspace_bytes(M, N, K, rt, bwd);
+    memset(&b, 0, sizeof(b));
     WsCarve c{static_cast<char*>(ws), 0};
+    if (!bwd && M <= kGatedSmall) {
+        b.sU = rt > 0 ? static_cast<uint16_t*>(c.take((size_t)M * rt * 2)) : nullptr;
+        b.part_floats = (size_t)kSms * 2 * M * 256;
+        b.part = static_cast<float*>(c.take(b.part_floats * 4));
+        b.counters = static_cast<unsigned long long*>(c.take((size_t)(N / 256) * 8));
+        b.bytes = c.used;
+        return b;
+    }
+    b.linear_bytes = linear_workspace_bytes(M, N, K, rt, bwd);
     b.linear = c.take(b.linear_bytes);
-    b.gu = gated && (bwd || M <= kSmallM) ? static_cast<uint16_t*>(c.take((size_t)M * N * 2)) : nullptr;
-    b.grad_part = nullptr;
-    if (gated && bwd && rt > 0) {
+    if (bwd) {
+        b.gu = static_cast<uint16_t*>(c.take((size_t)M * N * 2));
         const int S = gated_splits(M, N / 2);
-        const size_t tiles = (size_t)((M + 127) / 128);
-        if (S > 1) b.grad_part = static_cast<float*>(c.take(tiles * S * 128 * rt * 4));
+        if (rt > 0 && S > 1)
+            b.grad_part = static_cast<float*>(c.take((size_t)((M + 127) / 128) * S * 128 * rt * 4));
     }
     b.bytes = c.used;
     return b;
 }
 
+template <int TOK>
+inline cudaError_t launch_gated_small_kernel(const GatedSmallParams& p, int grid, cudaStream_t s) {
+    using S = GatedSmallShape<TOK>;
+    auto kern = k_gated_small<TOK>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    if (e != cudaSuccess) return e;
+    ProfileScope ps(QLORA_KERNEL_SMALLM_GEMM, s);
+    note_launch();
+    return launch_pdl(kern, dim3((unsigned)grid, 1, 1), dim3(S::THREADS, 1, 1), S::SMEM, s, 0, p);
+}
+
+// H = act(g) u for M <= kGatedSmall on a persistent stream-K grid (one CTA per
+// SM, at least four units per CTA).
+inline qlora_status gated_fwd_small(const void* X, const LinearArgs& a, const void* A, const void* B, int act, void* H,
+                                    void* GU, const BlockWs& b, cudaStream_t s) {
+    const qlora_nf4_weight& w = *a.w;
+    const int TOK = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;
+    GatedSmallParams p;
+    memset(&p, 0, sizeof(p));
+    if (!map_codes(&p.tmCodes, w, 32, 128)) return QLORA_ERR_CUDA;
+    if (!map_bf16(&p.tmX, X, a.K, a.M, TOK)) return QLORA_ERR_CUDA;
+    p.tmB = p.tmU = p.tmX;
+    if (a.r > 0) {
+        SkinnyDesc d;
+        if (!desc_sU(&d, X, a, A, b.sU)) return QLORA_ERR_CUDA;
+        const qlora_status st = skinny(&d, 1, a.rt(), s, 1);
+        if (st != QLORA_OK) return st;
+        if (!map_bf16(&p.tmB, B, a.r, a.N, 128)) return QLORA_ERR_CUDA;
+        if (!map_bf16(&p.tmU, b.sU, a.rt(), a.M, TOK)) return QLORA_ERR_CUDA;
+    }
+    p.q8 = w.absmax_q8;
+    p.c1 = w.absmax_scale;
+    p.offset = w.absmax_offset;
+    p.absmax = w.absmax;
+    p.dq = w.double_quant;
+    p.fmt = weight_format(w);
+    p.F = (int)a.seg_rows;
+    p.M = (int)a.M;
+    p.kbs = p.ks_main = (int)(a.K / 64);
+    p.ks_lora = a.r > 0 ? ceil_div(a.rt(), 64) : 0;
+    p.tiles = ceil_div(a.seg_rows, 128);
+    p.r = a.r;
+    p.act = act;
+    p.H = static_cast<uint16_t*>(H);
+    p.GU = static_cast<uint16_t*>(GU);
+    p.part = b.part;
+    p.part_cap = (int64_t)b.part_floats;
+    p.counters = b.counters;
+    p.epoch = next_epoch();
+    p.timeout_ns = wait_timeout_ns();
+    p.inject = inject_mode() == 1 ? 1 : 0;
+    const int64_t units = (int64_t)p.tiles * (p.ks_main + p.ks_lora);
+    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(sm_count(), kSms), units / 4));
+    const cudaError_t e = TOK == 16   ? launch_gated_small_kernel<16>(p, grid, s)
+                          : TOK == 32 ? launch_gated_small_kernel<32>(p, grid, s)
+                          : TOK == 64 ? launch_gated_small_kernel<64>(p, grid, s)
+                                      : launch_gated_small_kernel<128>(p, grid, s);
+    return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+}
+
 inline qlora_status gated_fwd_impl(const void* X, const LinearArgs& a, const void* A, const void* B, int act,
                                    void* H, void* GU, void* ws, cudaStream_t s) {
-    const BlockWs b = carve_block_ws(ws, a.M, a.N, a.K, a.rt(), 0, 1);
-    if (a.M > kSmallM) return gated_fwd_large(X, a, A, B, act, H, GU, b.linear, s);
-    uint16_t* gu = GU ? static_cast<uint16_t*>(GU) : b.gu;
-    const qlora_status st = linear_fwd_impl(X, a, A, B, gu, b.linear, b.linear_bytes, s);
-    if (st != QLORA_OK) return st;
-    note_launch();
-    const cudaError_t e = launch_pdl(k_gated_act, dim3(elementwise_grid(a.M * a.seg_rows / 8)), dim3(256), 0, s, 0,
-                                     (const uint16_t*)gu, static_cast<uint16_t*>(H), a.M, a.seg_rows, act);
-    return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+    const BlockWs b = carve_block_ws(ws, a.M, a.N, a.K, a.rt(), 0);
+    if (a.M <= kGatedSmall) return gated_fwd_small(X, a, A, B, act, H, GU, b, s);
+    return gated_fwd_large(X, a, A, B, act, H, GU, b.linear, s);
 }
 
 template <int BN>
@@ -1114,7 +1183,7 @@ inline qlora_status launch_gated_grad(const void* dH, const void* GU, const Line
 
 inline qlora_status gated_bwd_impl(const void* dH, const void* X, const void* GU, LinearArgs a, const void* A,
                                    const void* B, int act, void* dX, void* dA, void* dB, void* ws, cudaStream_t s) {
-    const BlockWs b = carve_block_ws(ws, a.M, a.N, a.K, a.rt(), 1, 1);
+    const BlockWs b = carve_block_ws(ws, a.M, a.N, a.K, a.rt(), 1);
     if (a.M > 0) {
         const qlora_status st = launch_gated_grad(dH, GU, a, B, act, b, s);
         if (st != QLORA_OK) return st;

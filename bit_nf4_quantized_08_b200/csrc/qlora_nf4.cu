@@ -504,7 +504,7 @@ qlora_status qlora_fused_linear_dropout_bwd(const void* dY, const void* X, int64
 
 size_t qlora_gated_linear_workspace(int64_t M, const qlora_nf4_weight* w, int32_t r, int32_t bwd) {
     if (check_fused(M, w, 2, r) != QLORA_OK) return 0;
-    return carve_block_ws(nullptr, M, w->rows, w->cols, 2 * r, bwd ? 1 : 0, 1).bytes;
+    return carve_block_ws(nullptr, M, w->rows, w->cols, 2 * r, bwd ? 1 : 0).bytes;
 }
 
 qlora_status qlora_gated_linear_fwd(const void* X, int64_t M, const qlora_nf4_weight* w, const void* A,
@@ -519,7 +519,7 @@ qlora_status qlora_gated_linear_fwd(const void* X, int64_t M, const qlora_nf4_we
     if (st != QLORA_OK || M == 0) return st;
     if (!X || !aligned(X, 16) || !H || !aligned(H, 16) || !aligned(GU, 16) || !adapter_ok(A, B, r))
         return QLORA_ERR_INVALID_ARG;
-    const size_t need = carve_block_ws(nullptr, M, w->rows, w->cols, 2 * r, 0, 1).bytes;
+    const size_t need = carve_block_ws(nullptr, M, w->rows, w->cols, 2 * r, 0).bytes;
     if (!ws || !aligned(ws, 16) || ws_bytes < need) return QLORA_ERR_INVALID_ARG;
     LinearArgs a{M, w->rows, w->cols, r, dropped_scale(scale, d), w, 2, w->rows / 2,
                  d.thr && r > 0 ? &d : nullptr, 0, 0, nullptr};
@@ -540,7 +540,7 @@ qlora_status qlora_gated_linear_bwd(const void* dH, const void* X, const void* G
     if (!adapter_ok(A, B, r) || !grads_ok(dA, dB, r)) return QLORA_ERR_INVALID_ARG;
     if (M > 0 && (!dH || !aligned(dH, 16) || !X || !aligned(X, 16) || !GU || !aligned(GU, 16) || !aligned(dX, 16)))
         return QLORA_ERR_INVALID_ARG;
-    const size_t need = carve_block_ws(nullptr, M, w->rows, w->cols, 2 * r, 1, 1).bytes;
+    const size_t need = carve_block_ws(nullptr, M, w->rows, w->cols, 2 * r, 1).bytes;
     if (!ws || !aligned(ws, 16) || ws_bytes < need) return QLORA_ERR_INVALID_ARG;
     if (!dX && r == 0) return QLORA_OK;  // nothing asked for
     LinearArgs a{M, w->rows, w->cols, r, dropped_scale(scale, d), w, 2, w->rows / 2,
