@@ -21,10 +21,10 @@
 // arrives last (an integer counter with a launch epoch) adds them in CTA order
 // (deterministic) and forms H.  Nothing waits on another CTA.
 //
-// Roles: warp 0 issues the TMA loads (codes, X or sU), warp 1 the MMAs, warps
-// 2-5 drain the accumulators (double-buffered in TMEM), and two groups of
-// eight dequant warps expand alternate units, one thread per weight row, the
-// block constants straight from the 8-bit codes two visits ahead.
+// Roles: warp 0 loads the codes and warp 6 the token tiles (X or sU) with TMA,
+// warp 1 issues the MMAs, warps 2-5 drain the accumulators (double-buffered in
+// TMEM), and two groups of eight dequant warps expand alternate units, one thread per weight row, the
+// block constants straight from the 8-bit codes.
 #pragma once
 
 #include "common.cuh"
@@ -60,52 +60,53 @@ struct GatedSmallParams {
 
 template <int TOK>
 struct GatedSmallShape {
+    // Two rings: code stages (released by the dequant warps) and operand slots, the expanded rows or the adapters' B
+    // rows and the token tile, released together by one tcgen05.commit.
     static constexpr int NG = 2;                     // dequant groups
+    static constexpr int CODE_BYTES = 256 * 32;      // 256 weight rows x 64 codes
+    static constexpr int C_STAGES = TOK <= 32 ? 8 : TOK <= 64 ? 6 : 8;
     static constexpr int B_BYTES = 256 * 128;        // 256 weight rows x 64 k bf16
-    static constexpr int B_SLOTS = TOK <= 32 ? 4 : 3;
-    static constexpr int CODE_BYTES = 256 * 32;
     static constexpr int X_BYTES = TOK * 128;
-    static constexpr int T_BYTES = CODE_BYTES + X_BYTES;
-    static constexpr int T_STAGES = TOK <= 16 ? 8 : TOK <= 32 ? 7 : TOK <= 64 ? 6 : 4;
-    // A group's wait for a stage's phase must never find the phase before it
-    // open: either the group meets the stage every time, or the stage's last
-    // unit lies behind one whose products the group has waited for.
-    static_assert(T_STAGES % NG == 0 || T_STAGES >= NG + B_SLOTS, "phase parities");
-    static constexpr int T_OFF = B_BYTES * B_SLOTS;
-    // the products read 128 token rows from the last stage's X tile on
-    static constexpr int T_END = T_OFF + T_BYTES * T_STAGES + (128 - TOK) * 128;
-    static constexpr int T8_OFF = T_END;
+    static constexpr int SLOT = B_BYTES + X_BYTES;
+    static constexpr int SLOTS = TOK <= 64 ? 4 : 3;
+    static constexpr int C_OFF = SLOT * SLOTS;       // (the last slot's products read up to 14 KB past it)
+    static constexpr int T8_OFF = C_OFF + CODE_BYTES * C_STAGES;
     static constexpr int BAR_OFF = T8_OFF + 1024;
     static constexpr int SMEM = BAR_OFF + 512 + 1024;
-    static constexpr int FIRST_DQ_WARP = 6;
+    static constexpr int FIRST_DQ_WARP = 8;
     static constexpr int THREADS = 32 * (FIRST_DQ_WARP + 8 * NG);
     static_assert(SMEM <= 232448, "shared memory per CTA");
+    static_assert(CODE_BYTES * C_STAGES >= (128 - TOK) * 128, "rows past the last token tile are readable");
+    // A group's wait for a phase of a stage or slot must never find the phase
+    // before it open: it meets the same stages every time, and the slot's use
+    // before last lies behind products that it has waited for.
+    static_assert(C_STAGES % NG == 0 && SLOTS >= NG, "phase parities");
 };
 
 template <int TOK>
 __global__ void __launch_bounds__(GatedSmallShape<TOK>::THREADS, 1)
     k_gated_small(const __grid_constant__ GatedSmallParams p) {
     using S = GatedSmallShape<TOK>;
-    constexpr int TS = S::T_STAGES, BS = S::B_SLOTS, NG = S::NG;
+    constexpr int CS = S::C_STAGES, BS = S::SLOTS, NG = S::NG;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_base = smem_u32(smem_raw);
     const uint32_t base = (raw_base + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - raw_base);
     float* t8s = reinterpret_cast<float*>(gbase + S::T8_OFF);
-    auto slotB = [&](int a) { return base + (uint32_t)(a * S::B_BYTES); };
-    auto stC = [&](int s) { return base + (uint32_t)(S::T_OFF + s * S::T_BYTES); };
-    auto stX = [&](int s) { return base + (uint32_t)(S::T_OFF + s * S::T_BYTES + S::CODE_BYTES); };
+    auto slotB = [&](int a) { return base + (uint32_t)(a * S::SLOT); };
+    auto slotX = [&](int a) { return base + (uint32_t)(a * S::SLOT + S::B_BYTES); };
+    auto stC = [&](int s) { return base + (uint32_t)(S::C_OFF + s * S::CODE_BYTES); };
     const uint32_t bar = base + S::BAR_OFF;
-    auto full_tma = [&](int s) { return bar + 8u * s; };
-    auto empty_tma = [&](int s) { return bar + 8u * (TS + s); };
-    auto b_full = [&](int a) { return bar + 8u * (2 * TS + a); };
-    auto b_empty = [&](int a) { return bar + 8u * (2 * TS + BS + a); };
-    auto acc_full = [&](int b) { return bar + 8u * (2 * TS + 2 * BS + b); };
-    auto acc_empty = [&](int b) { return bar + 8u * (2 * TS + 2 * BS + 2 + b); };
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(gbase + S::BAR_OFF + 8 * (2 * TS + 2 * BS + 4));
+    auto c_full = [&](int s) { return bar + 8u * s; };
+    auto c_empty = [&](int s) { return bar + 8u * (CS + s); };
+    auto b_full = [&](int a) { return bar + 8u * (2 * CS + a); };
+    auto b_empty = [&](int a) { return bar + 8u * (2 * CS + BS + a); };
+    auto acc_full = [&](int b) { return bar + 8u * (2 * CS + 2 * BS + b); };
+    auto acc_empty = [&](int b) { return bar + 8u * (2 * CS + 2 * BS + 2 + b); };
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(gbase + S::BAR_OFF + 8 * (2 * CS + 2 * BS + 4));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     volatile int* last_flag = reinterpret_cast<volatile int*>(tmem_holder + 2);
-    static_assert(8 * (2 * TS + 2 * BS + 4) + 16 <= 512, "barriers");
+    static_assert(8 * (2 * CS + 2 * BS + 4) + 16 <= 512, "barriers");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const WaitCfg wc{p.timeout_ns};
@@ -117,12 +118,12 @@ __global__ void __launch_bounds__(GatedSmallShape<TOK>::THREADS, 1)
     const int nunits = (int)(r_end - r_begin);
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < TS; ++s) {
-            mbar_init(full_tma(s), 1);
-            mbar_init(empty_tma(s), 1);
+        for (int s = 0; s < CS; ++s) {
+            mbar_init(c_full(s), 1);
+            mbar_init(c_empty(s), 8);  // the eight warps of the unit's dequant group
         }
         for (int a = 0; a < BS; ++a) {
-            mbar_init(b_full(a), 8);  // the eight warps of the unit's dequant group
+            mbar_init(b_full(a), 9);  // those warps, and the loads of the token tile
             mbar_init(b_empty(a), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -155,29 +156,20 @@ __global__ void __launch_bounds__(GatedSmallShape<TOK>::THREADS, 1)
     if (p.ks_lora == 0) pdl_wait();
 
     if (warp == 0) {
-        // ------------------------------------------------------------ producer
+        // ------------------------------------------------------------ code producer
         if (lane == 0 && !p.inject) {
-            bool waited = false;
-            int last_use[TS];
-            for (int s = 0; s < TS; ++s) last_use[s] = -1;
+            int last_use[CS];
+            for (int s = 0; s < CS; ++s) last_use[s] = -1;
             int tile = (int)(r_begin / KS), k = (int)(r_begin - (int64_t)tile * KS);
             for (int it = 0; it < nunits; ++it) {
-                const int s = it % TS, u = it / TS;
-                if (!mbar_wait(empty_tma(s), (u & 1) ^ 1, wc)) { *abort_flag = 1; break; }
+                const int s = it % CS, u = it / CS;
+                if (!mbar_wait_hint(c_empty(s), (u & 1) ^ 1, wc, 1000)) { *abort_flag = 1; break; }
                 if (k < p.ks_main) {
-                    mbar_arrive_expect_tx(full_tma(s), S::CODE_BYTES + S::X_BYTES);
-                    tma_load_2d(stC(s), &p.tmCodes, full_tma(s), k * 32, tile * 128);
-                    tma_load_2d(stC(s) + S::CODE_BYTES / 2, &p.tmCodes, full_tma(s), k * 32, p.F + tile * 128);
-                    tma_load_2d(stX(s), &p.tmX, full_tma(s), k * 64, 0);
+                    mbar_arrive_expect_tx(c_full(s), S::CODE_BYTES);
+                    tma_load_2d(stC(s), &p.tmCodes, c_full(s), k * 32, tile * 128);
+                    tma_load_2d(stC(s) + S::CODE_BYTES / 2, &p.tmCodes, c_full(s), k * 32, p.F + tile * 128);
                 } else {
-                    // adapter step: the sU tile here; the B rows are loaded
-                    // into the unit's slot by its dequant group
-                    if (!waited) {
-                        pdl_wait();
-                        waited = true;
-                    }
-                    mbar_arrive_expect_tx(full_tma(s), S::X_BYTES);
-                    tma_load_2d(stX(s), &p.tmU, full_tma(s), (k - p.ks_main) * 64, 0);
+                    mbar_arrive(c_full(s));  // an adapter step has no codes
                 }
                 last_use[s] = u;
                 if (++k == KS) {
@@ -185,15 +177,56 @@ __global__ void __launch_bounds__(GatedSmallShape<TOK>::THREADS, 1)
                     ++tile;
                 }
             }
-            for (int s = 0; s < TS; ++s)
-                if (last_use[s] >= 0) mbar_wait(full_tma(s), last_use[s] & 1, wc);
+            for (int s = 0; s < CS; ++s)
+                if (last_use[s] >= 0) mbar_wait(c_full(s), last_use[s] & 1, wc);
+        }
+    } else if (warp == 6) {
+        // ------------------------------------------------------------ producer of the token tiles and B rows
+        if (lane == 0 && !p.inject) {
+            bool waited = false;
+            int last_use[BS];
+            for (int a = 0; a < BS; ++a) last_use[a] = -1;
+            int tile = (int)(r_begin / KS), k = (int)(r_begin - (int64_t)tile * KS);
+            for (int it = 0; it < nunits; ++it) {
+                const int a = it % BS, u = it / BS;
+                if (!mbar_wait_hint(b_empty(a), (u & 1) ^ 1, wc, 1000)) { *abort_flag = 1; break; }
+                if (k < p.ks_main) {
+                    mbar_arrive_expect_tx(b_full(a), S::X_BYTES);
+                    tma_load_2d(slotX(a), &p.tmX, b_full(a), k * 64, 0);
+                } else {
+                    // adapter step: sU, from the kernel before this one, and
+                    // the B rows in place of the expanded weight.  The up
+                    // rows' columns are shifted by r, and the loads' zero fill
+                    // makes the block-diagonal operand against [U_gate | U_up].
+                    if (!waited) {
+                        pdl_wait();
+                        waited = true;
+                    }
+                    const int x = (k - p.ks_main) * 64;
+                    mbar_arrive_expect_tx(b_full(a), S::X_BYTES + S::B_BYTES);
+                    tma_load_2d(slotX(a), &p.tmU, b_full(a), x, 0);
+                    tma_load_2d(slotB(a), &p.tmB, b_full(a), x, tile * 128);
+                    tma_load_2d(slotB(a) + S::B_BYTES / 2, &p.tmB, b_full(a), x - p.r, p.F + tile * 128);
+                }
+                last_use[a] = u;
+                if (++k == KS) {
+                    k = 0;
+                    ++tile;
+                }
+            }
+            // every load has landed before the CTA exits (after an abort this
+            // may run into its bound: the phase needs the dequant warps too)
+            for (int a = 0; a < BS; ++a)
+                if (last_use[a] >= 0) mbar_wait(b_full(a), last_use[a] & 1, wc);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         if (lane == 0) {
             constexpr uint32_t idesc = idesc_bf16_f32(128, 256, 0, 0);
+            const uint64_t xd0 = smem_desc_sw128(slotX(0), 16, 1024), bd0 = smem_desc_sw128(slotB(0), 16, 1024);
             bool ok = true;
             int seg = 0, it = 0;
+            uint32_t a = 0, ph = 0;  // slot and phase of unit it
             while (ok && it < nunits) {
                 const int64_t unit0 = r_begin + it;
                 const int k0 = (int)(unit0 % KS);
@@ -204,23 +237,26 @@ __global__ void __launch_bounds__(GatedSmallShape<TOK>::THREADS, 1)
                     *abort_flag = 1;
                 }
                 tc_fence_after();
+                const uint32_t acc = tmem + (uint32_t)(ab * 256);
                 for (int j = 0; ok && j < len; ++j, ++it) {
-                    const int s = it % TS, a = it % BS;
-                    if (!mbar_wait(b_full(a), (it / BS) & 1, wc)) { ok = false; *abort_flag = 1; break; }
+                    if (!mbar_wait(b_full((int)a), ph, wc)) { ok = false; *abort_flag = 1; break; }
                     tc_fence_after();
+                    const uint64_t so = (uint64_t)(a * (uint32_t)(S::SLOT >> 4));
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma_bf16(tmem + (uint32_t)(ab * 256), smem_desc_sw128(stX(s) + kk * 32, 16, 1024),
-                                  smem_desc_sw128(slotB(a) + kk * 32, 16, 1024), idesc, (j > 0 || kk > 0) ? 1u : 0u);
-                    umma_commit(b_empty(a));
-                    umma_commit(empty_tma(s));
+                    for (uint32_t kk = 0; kk < 4; ++kk)
+                        umma_bf16(acc, xd0 + so + 2 * kk, bd0 + so + 2 * kk, idesc, (j > 0 || kk > 0) ? 1u : 0u);
+                    umma_commit(b_empty((int)a));
+                    if (++a == (uint32_t)BS) {
+                        a = 0;
+                        ph ^= 1u;
+                    }
                 }
                 umma_commit(acc_full(ab));  // one phase per segment, also when cut short
                 ++seg;
             }
             if (!ok && seg > 0) mbar_wait(acc_full((seg - 1) & 1), ((seg - 1) >> 1) & 1, wc);
         }
-    } else if (warp < S::FIRST_DQ_WARP) {
+    } else if (warp < 6) {
         // ------------------------------------------------------------ epilogue
         const int quarter = warp & 3;
         const int m = quarter * 32 + lane;  // TMEM lane = token
@@ -345,7 +381,7 @@ __global__ void __launch_bounds__(GatedSmallShape<TOK>::THREADS, 1)
                 store_h(tok, tile * 128 + j, g, u);
             }
         }
-    } else {
+    } else if (warp >= S::FIRST_DQ_WARP) {
         // ------------------------------------------------------------ dequant groups
         const int dw = warp - S::FIRST_DQ_WARP;
         const int g = dw >> 3;               // this warp's group: units it with it % NG == g
@@ -354,77 +390,95 @@ __global__ void __launch_bounds__(GatedSmallShape<TOK>::THREADS, 1)
         const uint32_t code_off = sw32(t * 32), code_off2 = sw32(t * 32 + 16);
         const uint32_t out_off = t * 128;
         const float off = p.dq ? *p.offset : 0.0f;
-        struct Raw {
-            int q;    // q8 code, or -1 for an adapter step
-            float c;  // c1 (double quantization) or absmax
+        // Block constants of this thread's row, eight k-steps of one tile at a
+        // time: a window of the eight codes from the first one's block on
+        // (two aligned 8-byte loads and a funnel shift) and the c1 of its
+        // first and last block, loaded when the window before is taken up,
+        // about four visits before their use.  (One code a visit, loaded two
+        // visits ahead: its move to the next visit's register waited for the
+        // load, and the dequant warps spent 43 % of their time there.)
+        struct Window {
+            uint2 q;
+            float c_lo, c_hi;
+            int tile, kc;
         };
-        // raw block constant of the unit at (tile, k)
-        auto fetch = [&](bool on, int tile, int k) -> Raw {
-            Raw r{-1, 0.0f};
-            if (!on || k >= p.ks_main) return r;
-            const int64_t b = ((row0 + (int64_t)tile * 128) * p.kbs + k) >> p.fmt.bs_shift;
-            if (!p.dq) {
-                r.q = 0;
-                r.c = __ldg(p.absmax + b);
-            } else {
-                r.q = __ldg(p.q8 + b);
-                r.c = __ldg(p.c1 + (b >> 8));
-            }
-            return r;
-        };
-        struct Pos {
-            int tile, k;
-        };
-        auto advance = [&](Pos x) {
-            x.k += NG;
-            while (x.k >= KS) {
-                x.k -= KS;
-                ++x.tile;
-            }
+        const int sh = p.fmt.bs_shift;
+        const int64_t nblocks = ((int64_t)2 * p.F * p.kbs) >> sh;
+        auto first_block = [&](int tile, int kc) { return ((row0 + (int64_t)tile * 128) * p.kbs + 8 * kc) >> sh; };
+        auto load_window = [&](int tile, int kc) {
+            Window x;
+            x.tile = tile;
+            x.kc = kc;
+            const int64_t b = first_block(tile, kc), al = b & ~(int64_t)7;
+            const uint2 v0 = *reinterpret_cast<const uint2*>(p.q8 + al);
+            // (2F is a multiple of 512, so the codes are a whole number of words)
+            const uint2 v1 = al + 16 <= nblocks ? *reinterpret_cast<const uint2*>(p.q8 + al + 8) : make_uint2(0u, 0u);
+            const int off8 = (int)(b & 7);
+            const uint32_t w0 = off8 & 4 ? v0.y : v0.x, w1 = off8 & 4 ? v1.x : v0.y, w2 = off8 & 4 ? v1.y : v1.x;
+            x.q.x = __funnelshift_r(w0, w1, 8 * (off8 & 3));
+            x.q.y = __funnelshift_r(w1, w2, 8 * (off8 & 3));
+            x.c_lo = p.c1[b >> 8];
+            const int64_t b7 = b + 7 < nblocks ? b + 7 : nblocks - 1;
+            x.c_hi = p.c1[b7 >> 8];
             return x;
         };
-        Pos p0;
-        p0.tile = (int)((r_begin + g) / KS);
-        p0.k = (int)(r_begin + g - (int64_t)p0.tile * KS);
-        Pos p1 = advance(p0);
-        Raw r0 = fetch(g < nunits, p0.tile, p0.k), r1 = fetch(g + NG < nunits, p1.tile, p1.k);
+        // the window of this group's first unit past the window of (tile, k)
+        auto load_after = [&](int tile, int k) {
+            const int kc = k >> 3;
+            do {
+                k += NG;
+            } while (k < p.ks_main && (k >> 3) == kc);
+            while (k >= p.ks_main) {  // past the adapter steps, into the next tile
+                if (k >= KS) {
+                    k -= KS;
+                    ++tile;
+                } else {
+                    k += NG;
+                }
+            }
+            return tile < p.tiles ? load_window(tile, k >> 3) : Window{make_uint2(0u, 0u), 0.0f, 0.0f, -1, 0};
+        };
+        int tile = (int)((r_begin + g) / KS), k = (int)(r_begin + g - (int64_t)tile * KS);
+        Window cur{make_uint2(0u, 0u), 0.0f, 0.0f, -1, 0}, nxt = cur;
+        if (p.dq && g < nunits && k < p.ks_main) nxt = load_window(tile, k >> 3);
+        auto block_const = [&]() -> float {
+            const int64_t b = ((row0 + (int64_t)tile * 128) * p.kbs + k) >> sh;
+            if (!p.dq) return __ldg(p.absmax + b);
+            if (tile != cur.tile || (k >> 3) != cur.kc) {
+                cur = (tile == nxt.tile && (k >> 3) == nxt.kc) ? nxt : load_window(tile, k >> 3);
+                nxt = load_after(tile, k);
+            }
+            const int64_t b0 = first_block(cur.tile, cur.kc);
+            const int i = (int)(b - b0);
+            const uint32_t w = i & 4 ? cur.q.y : cur.q.x;
+            const float c1 = (int)(b0 & 255) + i >= 256 ? cur.c_hi : cur.c_lo;
+            return __fadd_rn(__fmul_rn(t8s[(w >> (8 * (i & 3))) & 255u], c1), off);
+        };
         bool dead = false;
-        for (int it = g; it < nunits; it += NG) {
-            const Raw rw = r0;
-            const Pos at = p0;
-            const Pos p2 = advance(p1);
-            r0 = r1;
-            r1 = fetch(it + 2 * NG < nunits, p2.tile, p2.k);
-            p0 = p1;
-            p1 = p2;
+        for (int it = g; it < nunits; it += NG, k += NG) {
+            while (k >= KS) {
+                k -= KS;
+                ++tile;
+            }
             if (dead) continue;
-            const int s = it % TS, a = it % BS;
-            if (!__all_sync(0xffffffffu, mbar_wait(full_tma(s), (it / TS) & 1, wc)) ||
-                !__all_sync(0xffffffffu, mbar_wait(b_empty(a), ((it / BS) & 1) ^ 1, wc))) {
+            const int s = it % CS, a = it % BS;
+            const bool weight = k < p.ks_main;
+            const float bc = weight ? block_const() : 0.0f;
+            if (!__all_sync(0xffffffffu, mbar_wait(c_full(s), (it / CS) & 1, wc))) {
                 *abort_flag = 1;
                 dead = true;
                 continue;
             }
-            if (at.k >= p.ks_main) {
-                // Adapter step: one thread loads the 256 B rows; its arrival
-                // carries the transaction bytes, the other warps arrive below.
-                // The up rows' columns are shifted by r, and the loads' zero
-                // fill makes the block-diagonal operand against [U_gate | U_up].
-                if ((dw & 7) == 0) {
-                    if (lane == 0) {
-                        const int x = (at.k - p.ks_main) * 64;
-                        mbar_arrive_expect_tx(b_full(a), S::B_BYTES);
-                        tma_load_2d(slotB(a), &p.tmB, b_full(a), x, at.tile * 128);
-                        tma_load_2d(slotB(a) + S::B_BYTES / 2, &p.tmB, b_full(a), x - p.r, p.F + at.tile * 128);
-                    }
-                    continue;
-                }
-            } else {
-                const uint32_t sB = slotB(a), sC = stC(s);
-                const uint4 c0 = ld_shared_v4(sC + code_off);
-                const uint4 c1 = ld_shared_v4(sC + code_off2);
+            if (!__all_sync(0xffffffffu, mbar_wait(b_empty(a), ((it / BS) & 1) ^ 1, wc))) {
+                *abort_flag = 1;
+                dead = true;
+                continue;
+            }
+            if (weight) {
+                const uint32_t sB = slotB(a);
+                const uint4 c0 = ld_shared_v4(stC(s) + code_off);
+                const uint4 c1 = ld_shared_v4(stC(s) + code_off2);
                 const uint32_t words[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-                const float bc = p.dq ? __fadd_rn(__fmul_rn(t8s[rw.q], rw.c), off) : rw.c;
                 const Nf4BlockTable tb = nf4_block_table(bc, p.fmt.code_type);
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
@@ -435,7 +489,12 @@ __global__ void __launch_bounds__(GatedSmallShape<TOK>::THREADS, 1)
                 fence_proxy_async_smem();
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(b_full(a));
+            // (the code stage is released only here, after the stores that
+            // depend on every read of it)
+            if (lane == 0) {
+                mbar_arrive(b_full(a));
+                mbar_arrive(c_empty(s));
+            }
         }
     }
 
