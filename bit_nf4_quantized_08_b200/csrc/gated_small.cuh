@@ -4,30 +4,27 @@
 //
 //   H = act(g) u,   [g | u] = X W'^T + sU B^T  (adapters of the two halves)
 //
-// The weight rows are the MMA's N side: a step is 128 gate rows and the 128
-// matching up rows of one 64-element block column as one 256-column operand
-// against up to 128 tokens, so that four 128 x 256 x 16 products (about 0.28
-// us) and one commit consume 16384 weights.  (With the weight rows on the
-// 128-row M side, as in the plain small-M linear, four issues and two commits
-// consume 8192 in about 0.45 us, whatever the token count.)  The token tile's
-// unused rows hold whatever follows it in shared memory; they only reach
-// accumulator rows that nobody reads.
+// The weight rows are the MMA's N side: a unit of work is (128 hidden columns,
+// one 64-element k-step), i.e. 128 gate rows and the 128 matching up rows as
+// one 256-column operand against up to 128 tokens, so that one step of four
+// 128 x 256 x 16 products (about 0.28 us) consumes 16384 weights.  (With the
+// weight rows on the 128-row M side, as in the plain small-M linear, the same
+// four issues and two commits consume 8192 in about 0.45 us, whatever the
+// token count: the issue cost of small products bounds that form.)  The token
+// tile's unused rows hold whatever follows it in shared memory; they only
+// reach accumulator rows that nobody reads.
 //
-// The unit of work is (128 hidden columns, four steps): one 128-byte line of
-// codes a weight row.  (Loaded as 32-byte lines a step, the ring alone, without
-// expansion and products, took 0.52 us a step.)  The units, tiles x QS with
-// QS = ceil(K/256) + ceil(2r/256), are split evenly over a persistent grid of
-// one CTA per SM (stream-K).  A tile's g and u sit in one accumulator, so a
-// CTA that holds a whole tile forms H from it; where a tile is cut between
-// CTAs each publishes its fp32 partial sums and the one that arrives last (an
-// integer counter with a launch epoch) adds them in CTA order (deterministic)
-// and forms H.  Nothing waits on another CTA.
+// The units, tiles x KS with KS = K/64 + ceil(2r/64), are split evenly over a
+// persistent grid of one CTA per SM (stream-K).  A tile's g and u sit in one
+// accumulator, so a CTA that holds a whole tile forms H from it; where a tile
+// is cut between CTAs each publishes its fp32 partial sums and the one that
+// arrives last (an integer counter with a launch epoch) adds them in CTA order
+// (deterministic) and forms H.  Nothing waits on another CTA.
 //
 // Roles: warp 0 loads the codes and warp 6 the token tiles (X or sU) with TMA,
 // warp 1 issues the MMAs, warps 2-5 drain the accumulators (double-buffered in
-// TMEM), and two groups of eight dequant warps expand alternate steps, one
-// thread per weight row, the block constants straight from the 8-bit codes,
-// four steps' at a time.
+// TMEM), and two groups of eight dequant warps expand alternate units, one thread per weight row, the
+// block constants straight from the 8-bit codes.
 #pragma once
 
 #include "common.cuh"
@@ -39,7 +36,7 @@
 namespace qlora {
 
 struct GatedSmallParams {
-    CUtensorMap tmCodes;  // codes [2F][K/2] bytes, box {128 B, 128 rows}, 128-byte swizzle
+    CUtensorMap tmCodes;  // codes [2F][K/2] bytes, box {32 B, 128 rows}, 32-byte swizzle
     CUtensorMap tmX;      // X [M][K] bf16, box {64, TOK}, 128-byte swizzle
     CUtensorMap tmB;      // B [2F][r] bf16, box {64, 128}, 128-byte swizzle
     CUtensorMap tmU;      // sU [M][2r] bf16, box {64, TOK}, 128-byte swizzle
@@ -49,7 +46,7 @@ struct GatedSmallParams {
     const float* absmax;  // without double quantization
     int dq;
     int F, M, kbs;        // kbs = K / 64
-    int ks_lora, tiles, r, act;  // ks_lora = ceil(2r / 64)
+    int ks_main, ks_lora, tiles, r, act;
     QFormat fmt;
     uint16_t* H;          // [M][F]
     uint16_t* GU;         // [M][2F] or nullptr
@@ -61,18 +58,39 @@ struct GatedSmallParams {
     int inject;
 };
 
+// nf4_block_table with a code book known at compile time.
+template <int CT>
+__device__ constexpr uint32_t code_bits_of(int j) {
+    constexpr uint32_t v[2][16] = {{QLORA_NF4_BITS}, {QLORA_FP4_BITS}};
+    return v[CT][j];
+}
+template <int CT>
+__device__ __forceinline__ Nf4BlockTable nf4_block_table_of(float a) {
+    uint32_t P[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        P[i] = pack_bf16x2(__fmul_rn(__uint_as_float(code_bits_of<CT>(2 * i)), a),
+                           __fmul_rn(__uint_as_float(code_bits_of<CT>(2 * i + 1)), a));
+    Nf4BlockTable t;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        t.L[q] = prmt(P[2 * q], P[2 * q + 1], 0x6420u);
+        t.H[q] = prmt(P[2 * q], P[2 * q + 1], 0x7531u);
+    }
+    return t;
+}
+
 template <int TOK>
 struct GatedSmallShape {
-    // Two rings: code stages of one unit (released by the dequant warps) and
-    // operand slots of one step, the expanded rows or the adapters' B rows and
-    // the token tile, released together by one tcgen05.commit.
-    static constexpr int NG = 2;                     // dequant groups
-    static constexpr int CODE_BYTES = 256 * 128;     // 256 weight rows x 256 codes
-    static constexpr int C_STAGES = 3;
+    // Two rings: code stages (released by the dequant warps) and operand slots, the expanded rows or the adapters' B
+    // rows and the token tile, released together by one tcgen05.commit.
+    static constexpr int NG = 3;                     // dequant groups
+    static constexpr int CODE_BYTES = 256 * 32;      // 256 weight rows x 64 codes
+    static constexpr int C_STAGES = 6;
     static constexpr int B_BYTES = 256 * 128;        // 256 weight rows x 64 k bf16
     static constexpr int X_BYTES = TOK * 128;
     static constexpr int SLOT = B_BYTES + X_BYTES;
-    static constexpr int SLOTS = TOK <= 64 ? 3 : 2;
+    static constexpr int SLOTS = TOK <= 64 ? 4 : 3;
     static constexpr int C_OFF = SLOT * SLOTS;       // (the last slot's products read up to 14 KB past it)
     static constexpr int T8_OFF = C_OFF + CODE_BYTES * C_STAGES;
     static constexpr int BAR_OFF = T8_OFF + 1024;
@@ -81,10 +99,10 @@ struct GatedSmallShape {
     static constexpr int THREADS = 32 * (FIRST_DQ_WARP + 8 * NG);
     static_assert(SMEM <= 232448, "shared memory per CTA");
     static_assert(CODE_BYTES * C_STAGES >= (128 - TOK) * 128, "rows past the last token tile are readable");
-    // A group's wait for a phase of a slot must never find the phase before it
-    // open: the slot's use before last lies behind products that the group has
-    // waited for.
-    static_assert(SLOTS >= NG, "phase parities");
+    // A group's wait for a phase of a stage or slot must never find the phase
+    // before it open: it meets the same stages every time, and the slot's use
+    // before last lies behind products that it has waited for.
+    static_assert(C_STAGES % NG == 0 && SLOTS >= NG, "phase parities");
 };
 
 template <int TOK>
@@ -114,22 +132,20 @@ __global__ void __launch_bounds__(GatedSmallShape<TOK>::THREADS, 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const WaitCfg wc{p.timeout_ns};
-    const int QW = (p.kbs + 3) >> 2, QS = QW + ((p.ks_lora + 3) >> 2);  // units of a tile: weight, then adapter steps
-    const int64_t I = (int64_t)p.tiles * QS;
+    const int KS = p.ks_main + p.ks_lora;
+    const int64_t I = (int64_t)p.tiles * KS;
     const int G = gridDim.x;
     const int64_t r_begin = I * blockIdx.x / G;
     const int64_t r_end = I * (blockIdx.x + 1) / G;
     const int nunits = (int)(r_end - r_begin);
-    // steps of unit q of a tile
-    auto steps = [&](int q) { return q < QW ? min(4, p.kbs - 4 * q) : min(4, p.ks_lora - 4 * (q - QW)); };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < CS; ++s) {
             mbar_init(c_full(s), 1);
-            mbar_init(c_empty(s), 8 * NG);  // every dequant warp
+            mbar_init(c_empty(s), 8);  // the eight warps of the unit's dequant group
         }
         for (int a = 0; a < BS; ++a) {
-            mbar_init(b_full(a), 9);  // the eight warps of the step's group, and the loads of the token tile
+            mbar_init(b_full(a), 9);  // those warps, and the loads of the token tile
             mbar_init(b_empty(a), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -166,20 +182,20 @@ __global__ void __launch_bounds__(GatedSmallShape<TOK>::THREADS, 1)
         if (lane == 0 && !p.inject) {
             int last_use[CS];
             for (int s = 0; s < CS; ++s) last_use[s] = -1;
-            int tile = (int)(r_begin / QS), q = (int)(r_begin - (int64_t)tile * QS);
-            for (int i = 0; i < nunits; ++i) {
-                const int s = i % CS, u = i / CS;
+            int tile = (int)(r_begin / KS), k = (int)(r_begin - (int64_t)tile * KS);
+            for (int it = 0; it < nunits; ++it) {
+                const int s = it % CS, u = it / CS;
                 if (!mbar_wait_hint(c_empty(s), (u & 1) ^ 1, wc, 1000)) { *abort_flag = 1; break; }
-                if (q < QW) {
+                if (k < p.ks_main) {
                     mbar_arrive_expect_tx(c_full(s), S::CODE_BYTES);
-                    tma_load_2d(stC(s), &p.tmCodes, c_full(s), q * 128, tile * 128);
-                    tma_load_2d(stC(s) + S::CODE_BYTES / 2, &p.tmCodes, c_full(s), q * 128, p.F + tile * 128);
+                    tma_load_2d(stC(s), &p.tmCodes, c_full(s), k * 32, tile * 128);
+                    tma_load_2d(stC(s) + S::CODE_BYTES / 2, &p.tmCodes, c_full(s), k * 32, p.F + tile * 128);
                 } else {
-                    mbar_arrive(c_full(s));  // adapter steps have no codes
+                    mbar_arrive(c_full(s));  // an adapter step has no codes
                 }
                 last_use[s] = u;
-                if (++q == QS) {
-                    q = 0;
+                if (++k == KS) {
+                    k = 0;
                     ++tile;
                 }
             }
@@ -189,49 +205,41 @@ __global__ void __launch_bounds__(GatedSmallShape<TOK>::THREADS, 1)
     } else if (warp == 6) {
         // ------------------------------------------------------------ producer of the token tiles and B rows
         if (lane == 0 && !p.inject) {
-            bool waited = false, ok = true;
+            bool waited = false;
             int last_use[BS];
             for (int a = 0; a < BS; ++a) last_use[a] = -1;
-            int tile = (int)(r_begin / QS), q = (int)(r_begin - (int64_t)tile * QS);
-            uint32_t a = 0, u = 0;  // slot and use of the step
-            for (int i = 0; ok && i < nunits; ++i) {
-                const int ns = steps(q);
-                for (int j = 0; j < ns; ++j) {
-                    if (!mbar_wait_hint(b_empty((int)a), (u & 1) ^ 1, wc, 1000)) { *abort_flag = 1; ok = false; break; }
-                    if (q < QW) {
-                        mbar_arrive_expect_tx(b_full((int)a), S::X_BYTES);
-                        tma_load_2d(slotX((int)a), &p.tmX, b_full((int)a), (4 * q + j) * 64, 0);
-                    } else {
-                        // adapter step: sU, from the kernel before this one,
-                        // and the B rows in place of the expanded weight.  The
-                        // up rows' columns are shifted by r, and the loads'
-                        // zero fill makes the block-diagonal operand against
-                        // [U_gate | U_up].
-                        if (!waited) {
-                            pdl_wait();
-                            waited = true;
-                        }
-                        const int x = (4 * (q - QW) + j) * 64;
-                        mbar_arrive_expect_tx(b_full((int)a), S::X_BYTES + S::B_BYTES);
-                        tma_load_2d(slotX((int)a), &p.tmU, b_full((int)a), x, 0);
-                        tma_load_2d(slotB((int)a), &p.tmB, b_full((int)a), x, tile * 128);
-                        tma_load_2d(slotB((int)a) + S::B_BYTES / 2, &p.tmB, b_full((int)a), x - p.r, p.F + tile * 128);
+            int tile = (int)(r_begin / KS), k = (int)(r_begin - (int64_t)tile * KS);
+            for (int it = 0; it < nunits; ++it) {
+                const int a = it % BS, u = it / BS;
+                if (!mbar_wait_hint(b_empty(a), (u & 1) ^ 1, wc, 1000)) { *abort_flag = 1; break; }
+                if (k < p.ks_main) {
+                    mbar_arrive_expect_tx(b_full(a), S::X_BYTES);
+                    tma_load_2d(slotX(a), &p.tmX, b_full(a), k * 64, 0);
+                } else {
+                    // adapter step: sU, from the kernel before this one, and
+                    // the B rows in place of the expanded weight.  The up
+                    // rows' columns are shifted by r, and the loads' zero fill
+                    // makes the block-diagonal operand against [U_gate | U_up].
+                    if (!waited) {
+                        pdl_wait();
+                        waited = true;
                     }
-                    last_use[a] = (int)u;
-                    if (++a == (uint32_t)BS) {
-                        a = 0;
-                        ++u;
-                    }
+                    const int x = (k - p.ks_main) * 64;
+                    mbar_arrive_expect_tx(b_full(a), S::X_BYTES + S::B_BYTES);
+                    tma_load_2d(slotX(a), &p.tmU, b_full(a), x, 0);
+                    tma_load_2d(slotB(a), &p.tmB, b_full(a), x, tile * 128);
+                    tma_load_2d(slotB(a) + S::B_BYTES / 2, &p.tmB, b_full(a), x - p.r, p.F + tile * 128);
                 }
-                if (++q == QS) {
-                    q = 0;
+                last_use[a] = u;
+                if (++k == KS) {
+                    k = 0;
                     ++tile;
                 }
             }
             // every load has landed before the CTA exits (after an abort this
             // may run into its bound: the phase needs the dequant warps too)
-            for (int s = 0; s < BS; ++s)
-                if (last_use[s] >= 0) mbar_wait(b_full(s), last_use[s] & 1, wc);
+            for (int a = 0; a < BS; ++a)
+                if (last_use[a] >= 0) mbar_wait(b_full(a), last_use[a] & 1, wc);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
@@ -239,40 +247,34 @@ __global__ void __launch_bounds__(GatedSmallShape<TOK>::THREADS, 1)
             constexpr uint32_t idesc = idesc_bf16_f32(128, 256, 0, 0);
             const uint64_t xd0 = smem_desc_sw128(slotX(0), 16, 1024), bd0 = smem_desc_sw128(slotB(0), 16, 1024);
             bool ok = true;
-            int seg = 0, q = (int)(r_begin % QS);
-            uint32_t a = 0, ph = 0;  // slot and phase of the step
-            bool first = true;       // of the segment
-            for (int i = 0; ok && i < nunits; ++i) {
+            int seg = 0, it = 0;
+            uint32_t a = 0, ph = 0;  // slot and phase of unit it
+            while (ok && it < nunits) {
+                const int64_t unit0 = r_begin + it;
+                const int k0 = (int)(unit0 % KS);
+                const int len = (int)min((int64_t)(KS - k0), (int64_t)(nunits - it));
                 const int ab = seg & 1;
-                if (first) {
-                    if (seg >= 2 && !mbar_wait(acc_empty(ab), ((seg >> 1) - 1) & 1, wc)) {
-                        ok = false;
-                        *abort_flag = 1;
-                    }
-                    tc_fence_after();
+                if (seg >= 2 && !mbar_wait(acc_empty(ab), ((seg >> 1) - 1) & 1, wc)) {
+                    ok = false;
+                    *abort_flag = 1;
                 }
+                tc_fence_after();
                 const uint32_t acc = tmem + (uint32_t)(ab * 256);
-                const int ns = steps(q);
-                for (int j = 0; ok && j < ns; ++j) {
+                for (int j = 0; ok && j < len; ++j, ++it) {
                     if (!mbar_wait(b_full((int)a), ph, wc)) { ok = false; *abort_flag = 1; break; }
                     tc_fence_after();
                     const uint64_t so = (uint64_t)(a * (uint32_t)(S::SLOT >> 4));
 #pragma unroll
                     for (uint32_t kk = 0; kk < 4; ++kk)
-                        umma_bf16(acc, xd0 + so + 2 * kk, bd0 + so + 2 * kk, idesc, (!first || kk > 0) ? 1u : 0u);
-                    first = false;
+                        umma_bf16(acc, xd0 + so + 2 * kk, bd0 + so + 2 * kk, idesc, (j > 0 || kk > 0) ? 1u : 0u);
                     umma_commit(b_empty((int)a));
                     if (++a == (uint32_t)BS) {
                         a = 0;
                         ph ^= 1u;
                     }
                 }
-                if (++q == QS || i == nunits - 1 || !ok) {
-                    umma_commit(acc_full(ab));  // one phase per segment, also when cut short
-                    ++seg;
-                    q = 0;
-                    first = true;
-                }
+                umma_commit(acc_full(ab));  // one phase per segment, also when cut short
+                ++seg;
             }
             if (!ok && seg > 0) mbar_wait(acc_full((seg - 1) & 1), ((seg - 1) >> 1) & 1, wc);
         }
@@ -287,8 +289,8 @@ __global__ void __launch_bounds__(GatedSmallShape<TOK>::THREADS, 1)
         auto store_h = [&](int tok, int f, const float (&g)[4], const float (&u)[4]) {  // four hidden columns
             float h[4];
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
-                h[n] = (p.act == ACT_SILU ? act_value(ACT_SILU, g[n]) : act_value(ACT_GELU_TANH, g[n])) * u[n];
+            for (int i = 0; i < 4; ++i)
+                h[i] = (p.act == ACT_SILU ? act_value(ACT_SILU, g[i]) : act_value(ACT_GELU_TANH, g[i])) * u[i];
             if (!QLORA_CHECK(tok < p.M && f + 4 <= F)) return;
             *reinterpret_cast<uint2*>(p.H + (int64_t)tok * F + f) =
                 make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]));
@@ -300,14 +302,14 @@ __global__ void __launch_bounds__(GatedSmallShape<TOK>::THREADS, 1)
         };
         bool dead = false;
         int seg = 0;
-        for (int i = 0; i < nunits; ++seg) {
-            const int64_t unit0 = r_begin + i;
-            const int tile = (int)(unit0 / QS), k0 = (int)(unit0 - (int64_t)tile * QS);
-            const int len = (int)min((int64_t)(QS - k0), (int64_t)(nunits - i));
-            i += len;
+        for (int it = 0; it < nunits; ++seg) {
+            const int64_t unit0 = r_begin + it;
+            const int tile = (int)(unit0 / KS), k0 = (int)(unit0 - (int64_t)tile * KS);
+            const int len = (int)min((int64_t)(KS - k0), (int64_t)(nunits - it));
+            it += len;
             const int ab = seg & 1;
-            const bool whole = k0 == 0 && len == QS;
-            if (!dead && !__all_sync(0xffffffffu, mbar_wait(acc_full(ab), (seg >> 1) & 1, wc))) {
+            const bool whole = k0 == 0 && len == KS;
+            if (!dead && !__all_sync(0xffffffffu, mbar_wait_hint(acc_full(ab), (seg >> 1) & 1, wc, 4000))) {
                 *abort_flag = 1;
                 dead = true;
             }
@@ -350,8 +352,8 @@ __global__ void __launch_bounds__(GatedSmallShape<TOK>::THREADS, 1)
             if (whole) continue;
             // Part of a tile: the four warps meet whatever happened, so that
             // the named barriers are always met.
-            const int64_t t0 = (int64_t)tile * QS;
-            const int cf = owner_cta(t0, I, G), cl = owner_cta(t0 + QS - 1, I, G);  // (no share is empty)
+            const int64_t t0 = (int64_t)tile * KS;
+            const int cf = owner_cta(t0, I, G), cl = owner_cta(t0 + KS - 1, I, G);  // (no share is empty)
             __threadfence();
             named_bar(1, 128);
             if (et == 0) {
@@ -407,97 +409,102 @@ __global__ void __launch_bounds__(GatedSmallShape<TOK>::THREADS, 1)
         const int g = dw >> 3;               // this warp's group: units it with it % NG == g
         const int t = (dw & 7) * 32 + lane;  // weight row of the unit: 0..127 gate, 128..255 up
         const int64_t row0 = (t < 128 ? 0 : (int64_t)p.F - 128) + t;
-        const uint32_t code_row = (uint32_t)t * 128u, out_row = (uint32_t)t * 128u;
+        const uint32_t code_off = sw32(t * 32), code_off2 = sw32(t * 32 + 16);
+        const uint32_t row_x = (uint32_t)(t & 7) << 4, out_row = (uint32_t)t * 128u;
         const float off = p.dq ? *p.offset : 0.0f;
-        const int sh = p.fmt.bs_shift;
-        // Block constants of this thread's row for the steps of one unit: the
-        // codes of up to four blocks from the first one's on (two aligned
-        // words and a funnel shift) and the c1 of the first and the last,
-        // loaded a unit ahead.  (One code a step, loaded two steps ahead: its
-        // move to the next step's register waited for the load.)
-        struct Window {
-            uint32_t q;
-            float c_lo, c_hi;
-            int b;  // first block mod 256
+        const int sh = p.fmt.bs_shift, ct = p.fmt.code_type;
+        // Block constants of this thread's row.  Blocks of 64: the 8-bit codes
+        // by the aligned eight, the next eight loaded when these are taken up
+        // (nothing touches a loaded value before that), and one c1 for 256
+        // blocks; a new tile starts over.  Larger blocks, or fp32 constants:
+        // loaded at their use.
+        const int64_t nblocks = (int64_t)2 * p.F * p.kbs;  // (a multiple of 512)
+        const bool fast = p.dq && sh == 0;
+        int64_t wb = 0;  // first block of codes8
+        int pos = 0;     // this visit's block - wb
+        uint2 codes8 = make_uint2(0u, 0u), codes8_next = codes8;
+        float c1 = 0.0f;
+        auto load8 = [&](int64_t b) {
+            return b < nblocks ? *reinterpret_cast<const uint2*>(p.q8 + b) : make_uint2(0u, 0u);
         };
-        const int64_t nblocks = ((int64_t)2 * p.F * p.kbs) >> sh;  // (a multiple of 128)
-        auto load_window = [&](bool on, int64_t rb, int q) {
-            Window x{0u, 0.0f, 0.0f, 0};
-            if (!on || !p.dq || q >= QW) return x;
-            const int64_t b = (rb + 4 * q) >> sh, al = b & ~(int64_t)3;
-            const uint32_t v0 = *reinterpret_cast<const uint32_t*>(p.q8 + al);
-            const uint32_t v1 = al + 8 <= nblocks ? *reinterpret_cast<const uint32_t*>(p.q8 + al + 4) : 0u;
-            x.q = __funnelshift_r(v0, v1, 8 * (int)(b & 3));
-            x.c_lo = p.c1[b >> 8];
-            const int64_t b3 = b + 3 < nblocks ? b + 3 : nblocks - 1;
-            x.c_hi = p.c1[b3 >> 8];
-            x.b = (int)(b & 255);
-            return x;
+        auto start_row = [&](int64_t b) {
+            wb = b & ~(int64_t)7;
+            pos = (int)(b & 7);
+            codes8 = load8(wb);
+            codes8_next = load8(wb + 8);
+            c1 = p.c1[wb >> 8];
         };
-        int q = (int)(r_begin % QS);
-        int64_t rb = (row0 + r_begin / QS * 128) * p.kbs;  // first 64-element block of the row
-        Window cur, nxt = load_window(nunits > 0, rb, q);
-        bool dead = false;
-        uint32_t a = 0, u = 0, step = 0;  // slot and use of the step, step count
-        for (int i = 0; i < nunits; ++i) {
-            cur = nxt;
-            const int q0 = q;
-            const int64_t rb0 = rb;
-            if (++q == QS) {
-                q = 0;
-                rb += (int64_t)128 * p.kbs;
+        auto block_const = [&](int64_t blk64) -> float {
+            if (!fast) {
+                const int64_t b = blk64 >> sh;
+                if (!p.dq) return __ldg(p.absmax + b);
+                return __fadd_rn(__fmul_rn(t8s[__ldg(p.q8 + b)], __ldg(p.c1 + (b >> 8))), off);
             }
-            nxt = load_window(i + 1 < nunits, rb, q);
-            const int s = i % CS;
-            if (!dead && !__all_sync(0xffffffffu, mbar_wait(c_full(s), (i / CS) & 1, wc))) {
+            if (pos >= 8) {
+                pos -= 8;
+                wb += 8;
+                codes8 = codes8_next;
+                codes8_next = load8(wb + 8);
+                if ((wb & 255) == 0) c1 = p.c1[wb >> 8];
+            }
+            const uint32_t word = pos & 4 ? codes8.y : codes8.x;
+            return __fadd_rn(__fmul_rn(t8s[(word >> (8 * (pos & 3))) & 255u], c1), off);
+        };
+        int tile = (int)((r_begin + g) / KS), k = (int)(r_begin + g - (int64_t)tile * KS);
+        int64_t rb = (row0 + (int64_t)tile * 128) * p.kbs;  // the row's first 64-element block
+        int s = g % CS, sph = 0, a = g % BS, aph = 1;       // code stage, operand slot, parities to wait for
+        if (fast && g < nunits && k < p.ks_main) start_row(rb + k);
+        bool dead = false;
+        for (int it = g; it < nunits; it += NG) {
+            const bool weight = k < p.ks_main;
+            const float bc = weight ? block_const(rb + k) : 0.0f;
+            if (!dead && (!__all_sync(0xffffffffu, mbar_wait_hint(c_full(s), (uint32_t)sph, wc, 1000)) ||
+                          !__all_sync(0xffffffffu, mbar_wait_hint(b_empty(a), (uint32_t)aph, wc, 1000)))) {
                 *abort_flag = 1;
                 dead = true;
             }
-            const int ns = steps(q0);
-            const bool weight = q0 < QW;
-            for (int j = 0; j < ns; ++j, ++step) {
-                const uint32_t sl = a, use = u;
-                if (++a == (uint32_t)BS) {
-                    a = 0;
-                    ++u;
-                }
-                if (dead || (int)(step % NG) != g) continue;
-                Nf4BlockTable tb;
+            if (!dead) {
                 if (weight) {
-                    float bc;
-                    const int64_t b = (rb0 + 4 * q0 + j) >> sh;
-                    if (p.dq) {
-                        const int n = sh == 0 ? j : (int)(b - ((rb0 + 4 * q0) >> sh));
-                        const float c1 = cur.b + n >= 256 ? cur.c_hi : cur.c_lo;
-                        bc = __fadd_rn(__fmul_rn(t8s[(cur.q >> (8 * n)) & 255u], c1), off);
-                    } else {
-                        bc = __ldg(p.absmax + b);
-                    }
-                    tb = nf4_block_table(bc, p.fmt.code_type);
-                }
-                if (!__all_sync(0xffffffffu, mbar_wait(b_empty((int)sl), (use & 1) ^ 1, wc))) {
-                    *abort_flag = 1;
-                    dead = true;
-                    continue;
-                }
-                if (weight) {
-                    const uint32_t sB = slotB((int)sl), cr = stC(s) + code_row;
-                    const uint4 c0 = ld_shared_v4(cr + (uint32_t)(((2 * j) ^ (t & 7)) << 4));
-                    const uint4 c1 = ld_shared_v4(cr + (uint32_t)(((2 * j + 1) ^ (t & 7)) << 4));
-                    const uint32_t words[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+                    const uint32_t so = (slotB(a) + out_row) | row_x;  // (rows are 128-byte aligned)
+                    const uint4 c0 = ld_shared_v4(stC(s) + code_off);
+                    const uint4 c1v = ld_shared_v4(stC(s) + code_off2);
+                    const uint32_t words[8] = {c0.x, c0.y, c0.z, c0.w, c1v.x, c1v.y, c1v.z, c1v.w};
+                    const Nf4BlockTable tb = ct == 0 ? nf4_block_table_of<0>(bc) : nf4_block_table_of<1>(bc);
 #pragma unroll
-                    for (int n = 0; n < 8; ++n) {
+                    for (int q = 0; q < 8; ++q) {
                         uint32_t o[4];
-                        nf4_expand_word(words[n], tb, o);
-                        st_shared_v4(sB + out_row + (uint32_t)((n ^ (t & 7)) << 4), o[0], o[1], o[2], o[3]);
+                        nf4_expand_word(words[q], tb, o);
+                        st_shared_v4(so ^ (uint32_t)(q << 4), o[0], o[1], o[2], o[3]);
                     }
                     fence_proxy_async_smem();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(b_full((int)sl));
+                // (the code stage is released only here, after the stores that
+                // depend on every read of it)
+                if (lane == 0) {
+                    mbar_arrive(b_full(a));
+                    mbar_arrive(c_empty(s));
+                }
             }
-            // (released only here, after the stores that depend on every read)
-            if (lane == 0 && !dead) mbar_arrive(c_empty(s));
+            k += NG;
+            pos += NG;
+            if (k >= KS) {
+                do {
+                    k -= KS;
+                    rb += (int64_t)128 * p.kbs;
+                } while (k >= KS);
+                if (fast && it + NG < nunits && k < p.ks_main) start_row(rb + k);
+            }
+            s += NG;
+            if (s >= CS) {
+                s -= CS;
+                sph ^= 1;
+            }
+            a += NG;
+            if (a >= BS) {
+                a -= BS;
+                aph ^= 1;
+            }
         }
     }
 

@@ -1084,14 +1084,14 @@ inline cudaError_t launch_gated_small_kernel(const GatedSmallParams& p, int grid
 }
 
 // H = act(g) u for M <= kGatedSmall on a persistent stream-K grid (one CTA per
-// SM, at least one unit of four 64-element steps per CTA).
+// SM, at least four units per CTA).
 inline qlora_status gated_fwd_small(const void* X, const LinearArgs& a, const void* A, const void* B, int act, void* H,
                                     void* GU, const BlockWs& b, cudaStream_t s) {
     const qlora_nf4_weight& w = *a.w;
     const int TOK = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;
     GatedSmallParams p;
     memset(&p, 0, sizeof(p));
-    if (!map_codes(&p.tmCodes, w, 128, 128)) return QLORA_ERR_CUDA;
+    if (!map_codes(&p.tmCodes, w, 32, 128)) return QLORA_ERR_CUDA;
     if (!map_bf16(&p.tmX, X, a.K, a.M, TOK)) return QLORA_ERR_CUDA;
     p.tmB = p.tmU = p.tmX;
     if (a.r > 0) {
@@ -1110,7 +1110,7 @@ inline qlora_status gated_fwd_small(const void* X, const LinearArgs& a, const vo
     p.fmt = weight_format(w);
     p.F = (int)a.seg_rows;
     p.M = (int)a.M;
-    p.kbs = (int)(a.K / 64);
+    p.kbs = p.ks_main = (int)(a.K / 64);
     p.ks_lora = a.r > 0 ? ceil_div(a.rt(), 64) : 0;
     p.tiles = ceil_div(a.seg_rows, 128);
     p.r = a.r;
@@ -1123,8 +1123,8 @@ inline qlora_status gated_fwd_small(const void* X, const LinearArgs& a, const vo
     p.epoch = next_epoch();
     p.timeout_ns = wait_timeout_ns();
     p.inject = inject_mode() == 1 ? 1 : 0;
-    const int64_t units = (int64_t)p.tiles * (ceil_div(p.kbs, 4) + ceil_div(p.ks_lora, 4));
-    const int grid = (int)std::min<int64_t>(std::min(sm_count(), kSms), units);
+    const int64_t units = (int64_t)p.tiles * (p.ks_main + p.ks_lora);
+    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(sm_count(), kSms), units / 4));
     const cudaError_t e = TOK == 16   ? launch_gated_small_kernel<16>(p, grid, s)
                           : TOK == 32 ? launch_gated_small_kernel<32>(p, grid, s)
                           : TOK == 64 ? launch_gated_small_kernel<64>(p, grid, s)
