@@ -1083,6 +1083,22 @@ inline cudaError_t launch_gated_small_kernel(const GatedSmallParams& p, int grid
     return launch_pdl(kern, dim3((unsigned)grid, 1, 1), dim3(S::THREADS, 1, 1), S::SMEM, s, 0, p);
 }
 
+// sU for few tokens: k_small_u for up to 16 tokens without dropout, else the
+// skinny GEMM (128-token tiles, dropout).
+inline qlora_status launch_small_u(const void* X, const LinearArgs& a, const void* A, uint16_t* sU, cudaStream_t s) {
+    ProfileScope ps(QLORA_KERNEL_LORA_GEMM, s);
+    note_launch();
+    const cudaError_t e = launch_pdl(k_small_u, dim3((unsigned)(a.rt() / 8)), dim3(1024), 0, s, 0,
+                                     static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(A), sU, (int)a.M,
+                                     (int)a.K, a.rt(), a.scale);
+    return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+}
+inline qlora_status launch_sU(const void* X, const LinearArgs& a, const void* A, uint16_t* sU, cudaStream_t s) {
+    SkinnyDesc d;
+    if (!desc_sU(&d, X, a, A, sU)) return QLORA_ERR_CUDA;
+    return skinny(&d, 1, a.rt(), s, 1);
+}
+
 // H = act(g) u for M <= kGatedSmall on a persistent stream-K grid (one CTA per
 // SM, at least four units per CTA).
 inline qlora_status gated_fwd_small(const void* X, const LinearArgs& a, const void* A, const void* B, int act, void* H,
@@ -1095,9 +1111,7 @@ inline qlora_status gated_fwd_small(const void* X, const LinearArgs& a, const vo
     if (!map_bf16(&p.tmX, X, a.K, a.M, TOK)) return QLORA_ERR_CUDA;
     p.tmB = p.tmU = p.tmX;
     if (a.r > 0) {
-        SkinnyDesc d;
-        if (!desc_sU(&d, X, a, A, b.sU)) return QLORA_ERR_CUDA;
-        const qlora_status st = skinny(&d, 1, a.rt(), s, 1);
+        const qlora_status st = a.M <= 16 && !a.drop ? launch_small_u(X, a, A, b.sU, s) : launch_sU(X, a, A, b.sU, s);
         if (st != QLORA_OK) return st;
         if (!map_bf16(&p.tmB, B, a.r, a.N, 128)) return QLORA_ERR_CUDA;
         if (!map_bf16(&p.tmU, b.sU, a.rt(), a.M, TOK)) return QLORA_ERR_CUDA;
