@@ -8,6 +8,7 @@ allocation out of the timed region.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass
 
@@ -276,12 +277,17 @@ def _expect(t: torch.Tensor | None, name: str, shape, dtype, device, optional: b
         if optional:
             return
         raise ValueError(f"{name} is missing")
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _on(device):
+    """The device's guard, or nothing where it is the current one already."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 _GRAD_DTYPES = {torch.float32: QLORA_F32, torch.bfloat16: QLORA_BF16}
@@ -331,7 +337,7 @@ def qlora_dropout(X: torch.Tensor, dropout: Dropout, out: torch.Tensor | None = 
     if out is None:
         out = torch.empty_like(X)
     _expect(out, "out", X.shape, X.dtype, X.device)
-    with torch.cuda.device(X.device):
+    with _on(X.device):
         check(lib().qlora_dropout(_ptr(X), _GRAD_DTYPES[X.dtype], X.numel(), _drop_arg(dropout, X.device), _ptr(out),
                                   _stream()), "qlora_dropout")
     return out
@@ -353,7 +359,7 @@ def qlora_fused_linear_dropout_fwd(X: torch.Tensor, w: NF4Weight, nseg: int, A: 
     _expect(Y, "Y", (M, w.rows), torch.bfloat16, X.device)
     wsb = _workspace(qlora_fused_linear_dropout_workspace(M, w, nseg, r, False), X.device, ws)
     cw = w.c_struct()
-    with torch.cuda.device(X.device):
+    with _on(X.device):
         check(lib().qlora_fused_linear_dropout_fwd(_ptr(X), M, ctypes.byref(cw), nseg, _ptr(A), _ptr(B), r,
                                                    float(scale), _drop_arg(dropout, X.device), _ptr(Y), _ptr(wsb),
                                                    wsb.numel(), _stream()), "qlora_fused_linear_dropout_fwd")
@@ -376,7 +382,7 @@ def qlora_fused_linear_dropout_bwd(dY: torch.Tensor, X: torch.Tensor, w: NF4Weig
     dA, dB = _adapter_grads(dA, dB, nseg * r, w, r, grad_dtype, X.device)
     wsb = _workspace(qlora_fused_linear_dropout_workspace(M, w, nseg, r, True), X.device, ws)
     cw = w.c_struct()
-    with torch.cuda.device(X.device):
+    with _on(X.device):
         check(lib().qlora_fused_linear_dropout_bwd(
             _ptr(dY), _ptr(X), M, ctypes.byref(cw), nseg, _ptr(A), _ptr(B), r, float(scale),
             _drop_arg(dropout, X.device), _ptr(dX) if want_dx else None, _GRAD_DTYPES[grad_dtype], _ptr(dA), _ptr(dB),
@@ -412,7 +418,7 @@ def qlora_gated_linear_fwd(X: torch.Tensor, w: NF4Weight, A: torch.Tensor | None
     _expect(GU, "GU", (M, w.rows), torch.bfloat16, X.device, optional=True)
     wsb = _workspace(qlora_gated_linear_workspace(M, w, r, False), X.device, ws)
     cw = w.c_struct()
-    with torch.cuda.device(X.device):
+    with _on(X.device):
         check(lib().qlora_gated_linear_fwd(_ptr(X), M, ctypes.byref(cw), _ptr(A), _ptr(B), r, float(scale), _act(act),
                                            _drop_arg(dropout, X.device), _ptr(H), _ptr(GU), _ptr(wsb), wsb.numel(),
                                            _stream()), "qlora_gated_linear_fwd")
@@ -436,7 +442,7 @@ def qlora_gated_linear_bwd(dH: torch.Tensor, X: torch.Tensor, GU: torch.Tensor, 
     dA, dB = _adapter_grads(dA, dB, 2 * r, w, r, grad_dtype, X.device)
     wsb = _workspace(qlora_gated_linear_workspace(M, w, r, True), X.device, ws)
     cw = w.c_struct()
-    with torch.cuda.device(X.device):
+    with _on(X.device):
         check(lib().qlora_gated_linear_bwd(
             _ptr(dH), _ptr(X), _ptr(GU), M, ctypes.byref(cw), _ptr(A), _ptr(B), r, float(scale), _act(act),
             _drop_arg(dropout, X.device), _ptr(dX) if want_dx else None, _GRAD_DTYPES[grad_dtype], _ptr(dA), _ptr(dB),

@@ -709,55 +709,6 @@ inline qlora_status linear_fwd_impl(const void* X, const LinearArgs& a, const vo
     return launch_small_m(X, a, B, Y, L, s);
 }
 
-// H = act(g) u for M > kGatedSmall on the gated form of the pair kernel, one pair per
-// tile of 512 tokens x 128 hidden columns whatever schedule the linears use.
-inline qlora_status gated_fwd_large(const void* X, const LinearArgs& a, const void* A, const void* B, int act, void* H,
-                                    void* GU, void* ws, cudaStream_t s) {
-    const qlora_nf4_weight& w = *a.w;
-    const LinearWs L = carve_linear_ws(ws, a.M, a.N, a.K, a.rt(), 0);
-    if (launch_expand_scales(w, L.scales, L.scales_ld, s, nullptr, 0) != cudaSuccess) return QLORA_ERR_CUDA;
-    GemmParams p;
-    memset(&p, 0, sizeof(p));
-    if (!map_bf16(&p.tmA, X, a.K, a.M, 128)) return QLORA_ERR_CUDA;
-    p.tmB = p.tmA2 = p.tmB2 = p.tmA;
-    if (a.r > 0) {
-        SkinnyDesc d;
-        if (!desc_sU(&d, X, a, A, L.sU)) return QLORA_ERR_CUDA;
-        // beside the GEMM, as in linear_fwd_impl
-        const qlora_status st = skinny(&d, 1, a.rt(), s, 1, SKP_PACKED);
-        if (st != QLORA_OK) return st;
-        if (!map_bf16(&p.tmA2, L.sU, a.rt(), a.M, 128)) return QLORA_ERR_CUDA;
-        if (!map_bf16(&p.tmB2, B, a.r, a.N, 128)) return QLORA_ERR_CUDA;
-        p.ks_lora = ceil_div(a.rt(), 64);
-        p.lora_seg_r = a.r;
-        p.late_wait = 1;
-    }
-    if (!map_codes(&p.tmCodes, w, 32, 128)) return QLORA_ERR_CUDA;
-    const int64_t F = a.seg_rows;
-    if (!map_bf16(&p.tmOut, H, F, a.M, 128)) return QLORA_ERR_CUDA;
-    p.tmGU = p.tmOut;
-    if (GU && !map_bf16(&p.tmGU, GU, a.N, a.M, 128)) return QLORA_ERR_CUDA;
-    p.keep_gu = GU ? 1 : 0;
-    p.act = act;
-    p.gate_rows = (int)F;
-    p.scales = L.scales;
-    p.scales_ld = L.scales_ld;
-    p.code_type = w.code_type;
-    p.dq_rows = (int)a.N;
-    p.dq_kbs = (int)(a.K / 64);
-    p.ks_main = (int)(a.K / 64);
-    p.ks_per_split = p.ks_main;
-    p.rows = (int)a.M;
-    p.cols = (int)F;
-    p.out = H;
-    p.out_ld = F;
-    p.timeout_ns = wait_timeout_ns();
-    p.inject = inject_mode() == 1 ? 1 : 0;
-    const dim3 grid = grid_pair(p, ceil_div(F, 128), ceil_div(a.M, 512));
-    return launch_gemm_pair<DQ_B_K, 4, true>(p, grid, s, QLORA_KERNEL_FWD_GEMM) == cudaSuccess ? QLORA_OK
-                                                                                             : QLORA_ERR_CUDA;
-}
-
 // sG = bf16(scale dY B): Aop = dY [m][n] (K-major), Bop = B viewed [j][n] (MN-major).
 // (fused projection: sG = [dY_0 B_0 | dY_1 B_1 | ...], each k-step of dY rows
 // shifted onto its own segment's output columns)
@@ -1029,11 +980,14 @@ inline qlora_status linear_bwd_impl(const void* dY, const void* X, const LinearA
 }
 
 // ---------------------------------------------------------------------------
-// The gated feed-forward.  Workspace: backward and forward of more than
-// kGatedSmall tokens, the linear's; backward, then the gradient of the
-// pre-activations [M, 2F] and the split partial sums of sG; forward of few
-// tokens, sU, the partial tiles and their arrival counters.
+// The gated feed-forward.  Workspace: forward, sU and, for few tokens, the
+// partial tiles and their arrival counters, else the expanded block constants;
+// backward, the linear's, the gradient of the pre-activations [M, 2F] and the
+// split partial sums of sG.
 // ---------------------------------------------------------------------------
+// Most tokens of k_gated_small (its MMA's token side).  Around it, whole calls
+// with cold caches: LLaMA-7B 128 / 129 tokens 113 / 111 us, LLaMA-65B 186 /
+// 285 us; at 16 tokens 7B 50 us, 65B 133 us.
 constexpr int kGatedSmall = 128;
 
 struct BlockWs {
@@ -1042,6 +996,7 @@ struct BlockWs {
     uint16_t* gu;
     float* grad_part;
     uint16_t* sU;
+    float* scales;  // [K/64][N]
     float* part;
     size_t part_floats;
     unsigned long long* counters;
@@ -1060,14 +1015,17 @@ inline BlockWs carve_block_ws(void* ws, int64_t M, int64_t N, int64_t K, int rt,
         b.bytes = c.used;
         return b;
     }
+    if (!bwd) {
+        b.sU = rt > 0 ? static_cast<uint16_t*>(c.take((size_t)M * rt * 2)) : nullptr;
+        b.scales = static_cast<float*>(c.take((size_t)(K / 64) * N * 4));
+        b.bytes = c.used;
+        return b;
+    }
     b.linear_bytes = linear_workspace_bytes(M, N, K, rt, bwd);
     b.linear = c.take(b.linear_bytes);
-    if (bwd) {
-        b.gu = static_cast<uint16_t*>(c.take((size_t)M * N * 2));
-        const int S = gated_splits(M, N / 2);
-        if (rt > 0 && S > 1)
-            b.grad_part = static_cast<float*>(c.take((size_t)((M + 127) / 128) * S * 128 * rt * 4));
-    }
+    b.gu = static_cast<uint16_t*>(c.take((size_t)M * N * 2));
+    const int S = gated_splits(M, N / 2);
+    if (rt > 0 && S > 1) b.grad_part = static_cast<float*>(c.take((size_t)((M + 127) / 128) * S * 128 * rt * 4));
     b.bytes = c.used;
     return b;
 }
@@ -1146,11 +1104,59 @@ inline qlora_status gated_fwd_small(const void* X, const LinearArgs& a, const vo
     return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
+// H = act(g) u for M > kGatedSmall on the gated form of the pair kernel, one pair per
+// tile of 512 tokens x 128 hidden columns whatever schedule the linears use.
+inline qlora_status gated_fwd_large(const void* X, const LinearArgs& a, const void* A, const void* B, int act, void* H,
+                                    void* GU, const BlockWs& b, cudaStream_t s) {
+    const qlora_nf4_weight& w = *a.w;
+    if (launch_expand_scales(w, b.scales, a.N, s, nullptr, 0) != cudaSuccess) return QLORA_ERR_CUDA;
+    GemmParams p;
+    memset(&p, 0, sizeof(p));
+    if (!map_bf16(&p.tmA, X, a.K, a.M, 128)) return QLORA_ERR_CUDA;
+    p.tmB = p.tmA2 = p.tmB2 = p.tmA;
+    if (a.r > 0) {
+        SkinnyDesc d;
+        if (!desc_sU(&d, X, a, A, b.sU)) return QLORA_ERR_CUDA;
+        // beside the GEMM, as in linear_fwd_impl
+        const qlora_status st = skinny(&d, 1, a.rt(), s, 1, SKP_PACKED);
+        if (st != QLORA_OK) return st;
+        if (!map_bf16(&p.tmA2, b.sU, a.rt(), a.M, 128)) return QLORA_ERR_CUDA;
+        if (!map_bf16(&p.tmB2, B, a.r, a.N, 128)) return QLORA_ERR_CUDA;
+        p.ks_lora = ceil_div(a.rt(), 64);
+        p.lora_seg_r = a.r;
+        p.late_wait = 1;
+    }
+    if (!map_codes(&p.tmCodes, w, 32, 128)) return QLORA_ERR_CUDA;
+    const int64_t F = a.seg_rows;
+    if (!map_bf16(&p.tmOut, H, F, a.M, 128)) return QLORA_ERR_CUDA;
+    p.tmGU = p.tmOut;
+    if (GU && !map_bf16(&p.tmGU, GU, a.N, a.M, 128)) return QLORA_ERR_CUDA;
+    p.keep_gu = GU ? 1 : 0;
+    p.act = act;
+    p.gate_rows = (int)F;
+    p.scales = b.scales;
+    p.scales_ld = a.N;  // (2F is a multiple of 512)
+    p.code_type = w.code_type;
+    p.dq_rows = (int)a.N;
+    p.dq_kbs = (int)(a.K / 64);
+    p.ks_main = (int)(a.K / 64);
+    p.ks_per_split = p.ks_main;
+    p.rows = (int)a.M;
+    p.cols = (int)F;
+    p.out = H;
+    p.out_ld = F;
+    p.timeout_ns = wait_timeout_ns();
+    p.inject = inject_mode() == 1 ? 1 : 0;
+    const dim3 grid = grid_pair(p, ceil_div(F, 128), ceil_div(a.M, 512));
+    return launch_gemm_pair<DQ_B_K, 4, true>(p, grid, s, QLORA_KERNEL_FWD_GEMM) == cudaSuccess ? QLORA_OK
+                                                                                             : QLORA_ERR_CUDA;
+}
+
 inline qlora_status gated_fwd_impl(const void* X, const LinearArgs& a, const void* A, const void* B, int act,
                                    void* H, void* GU, void* ws, cudaStream_t s) {
     const BlockWs b = carve_block_ws(ws, a.M, a.N, a.K, a.rt(), 0);
     if (a.M <= kGatedSmall) return gated_fwd_small(X, a, A, B, act, H, GU, b, s);
-    return gated_fwd_large(X, a, A, B, act, H, GU, b.linear, s);
+    return gated_fwd_large(X, a, A, B, act, H, GU, b, s);
 }
 
 template <int BN>

@@ -280,3 +280,83 @@ def test_feed_forward_training_step(Q, O, cuda):
     big = np.abs(g) > 1e-4
     step = _np(p) - p0
     assert np.max(np.abs(step[big] + 1e-3 * np.sign(g[big]))) <= 1e-3 * 1e-3 + 2.0 ** -23 * np.max(np.abs(p0))
+
+
+@pytest.mark.parametrize("M", [30, 300])
+@pytest.mark.parametrize("p", [0.0, 0.3])
+def test_gated_backward_without_dx(Q, O, cuda, M, p):
+    """dA and dB alone (the first layer of a model): the bits of the whole backward's."""
+    q, inp, Wd = _setup(Q, M, 512, 320, 24, seed=18)
+    drop = Q.Dropout(p, 3, 1) if p else None
+    _, GU, g = _check(Q, O, q, inp, Wd, 2.0, "silu", drop, f"no dX M={M}", want_dx=False)
+    assert g[0] is None
+    t = _dev(inp)
+    Q.qlora_debug_inject(6)  # the same GEMM split (serial order), with dX
+    try:
+        full = Q.qlora_gated_linear_bwd(t["dH"], t["X"], GU, q, t["A"], t["B"], 2.0, "silu", drop)
+    finally:
+        Q.qlora_debug_inject(0)
+    torch.cuda.synchronize()
+    assert _same_bits(g[1], full[1]) and _same_bits(g[2], full[2])
+
+
+def test_gated_backward_in_a_capture_of_its_own(Q, cuda):
+    """Forward and backward captured and replayed on another stream than their inputs', twice, give the eager bits."""
+    M = 200
+    q, inp, _ = _setup(Q, M, 512, 256, 16, seed=19)
+    t = _dev(inp)
+    d = Q.Dropout(0.1, 2, 9)
+
+    def step():
+        H, GU = Q.qlora_gated_linear_fwd(t["X"], q, t["A"], t["B"], 2.0, "silu", d, want_gu=True)
+        return (H, GU, *Q.qlora_gated_linear_bwd(t["dH"], t["X"], GU, q, t["A"], t["B"], 2.0, "silu", d))
+
+    ref = [x.clone() for x in step()]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        out = step()
+    for _ in range(2):
+        for o in out:
+            o.fill_(0)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            g.replay()
+        torch.cuda.synchronize()
+        assert Q.qlora_get_last_error() == 0
+        assert all(_same_bits(a, b) for a, b in zip(out, ref))
+
+
+def test_waits_run_out_and_recover(Q, cuda):
+    """Without their producers' loads every kernel of the gated and dropout calls gives up after the bound, records
+    the timeout and returns; the next calls are right."""
+    sets = []
+    for M in (5, 100, 300):
+        q, inp, _ = _setup(Q, M, 512, 512, 16, seed=20)
+        sets.append((q, _dev(inp)))
+    d = Q.Dropout(0.2, 1, 1)
+
+    def calls(q, t):
+        H, GU = Q.qlora_gated_linear_fwd(t["X"], q, t["A"], t["B"], 2.0, "silu", d, want_gu=True)
+        g = Q.qlora_gated_linear_bwd(t["dH"], t["X"], GU, q, t["A"], t["B"], 2.0, "silu", d)
+        Y = Q.qlora_fused_linear_dropout_fwd(t["X"], q, 2, t["A"], t["B"], 2.0, d)
+        b = Q.qlora_fused_linear_dropout_bwd(Y, t["X"], q, 2, t["A"], t["B"], 2.0, d)
+        torch.cuda.synchronize()
+        return (H, GU, *g, Y, *b)
+
+    ref = [calls(*a) for a in sets]
+    assert Q.qlora_get_last_error() == 0
+    Q.qlora_set_wait_timeout_ns(5_000_000)
+    Q.qlora_debug_inject(1)
+    try:
+        for a in sets:
+            calls(*a)
+            assert Q.qlora_get_last_error() == Q.QLORA_ERR_TIMEOUT
+    finally:
+        Q.qlora_debug_inject(0)
+        Q.qlora_set_wait_timeout_ns(0)
+    for a, r in zip(sets, ref):
+        got = calls(*a)
+        assert Q.qlora_get_last_error() == 0
+        assert all(_same_bits(x, y) for x, y in zip(got, r))
