@@ -863,7 +863,7 @@ inline qlora_status linear_bwd_forked(const void* dY, const void* X, const Linea
     // pairs for a tile's time, about 0.85 us a k-step, against about 0.6 us
     // for each of the side launch's k-steps.  Measured with sU first / beside:
     // 4096 x 4096, r = 16, 2048 tokens (64 tiles) 96 / 100 us; LLaMA-7B q/k/v
-    // at 1531 tokens (48 tiles) 201 / 180 us.
+    // at 1531 tokens (48 tiles) 201 / 180 us (both with the expansion first).
     bool sU_first = a.drop && !a.have_sG;
     if (sU_first) {
         const int64_t pairs = kSms / 2, tiles = (int64_t)ceil_div(a.K, 256) * ceil_div(a.M, 512);
@@ -878,11 +878,17 @@ inline qlora_status linear_bwd_forked(const void* dY, const void* X, const Linea
         if (sU_first && !desc_sU(&d2[0], X, a, A, L.sU)) return QLORA_ERR_CUDA;
         st = skinny(d2, sU_first ? 2 : 1, a.rt(), s, 1, a.drop ? SKP_SPLIT : SKP_PACKED);
         if (st != QLORA_OK) return st;
+        // under dropout the dX GEMM waits for this launch in any case: the
+        // block constants are expanded beside it, not before it (every CTA of
+        // it waits for the call before, then lets the expansion start;
+        // 4096 x 4096 at 2048 tokens: 92 us instead of 96 us)
+        if (a.drop && launch_expand_scales(*a.w, L.scales, L.scales_ld, s, L.sk_flags, kMaxStreamK + 2, 1) != cudaSuccess)
+            return QLORA_ERR_CUDA;
     }
     if (cudaEventRecord(side.fork, s) != cudaSuccess) return QLORA_ERR_CUDA;
     if (cudaStreamWaitEvent(side.st, side.fork, 0) != cudaSuccess) return QLORA_ERR_CUDA;
     // from here on the side stream is joined back whatever happens
-    st = launch_dx_gemm(A, dX, a, L, tdY, a.have_sG ? 0 : 1, s);
+    st = launch_dx_gemm(A, dX, a, L, tdY, a.have_sG || a.drop ? 0 : 1, s);
     // sU, dA and dB in one persistent launch over every SM: the CTAs that
     // find an SM beside the GEMM take tiles from the shared counter while it
     // runs, the rest start as it ends.  sU tiles (inputs only) start at once,
@@ -891,10 +897,10 @@ inline qlora_status linear_bwd_forked(const void* dY, const void* X, const Linea
     if (st == QLORA_OK && !desc_sU(&d3[0], X, a, A, L.sU)) st = QLORA_ERR_CUDA;
     if (st == QLORA_OK && !desc_dA_dB(d3 + 1, dY, X, a, L, dA, dB)) st = QLORA_ERR_CUDA;
     // (have_sG: dY, sG and the zeroed counters come from the kernel before;
-    // sU_first: sU and sG do)
+    // dropout: sG, the counters and perhaps sU do)
     if (st == QLORA_OK)
         st = sU_first ? skinny(d3 + 1, 2, a.rt(), side.st, 1, SKP_STREAM, sm_count(), L.sk_flags + kMaxStreamK)
-                      : skinny(d3, 3, a.rt(), side.st, a.have_sG, SKP_STREAM, sm_count(), L.sk_flags + kMaxStreamK, 2,
+                      : skinny(d3, 3, a.rt(), side.st, a.have_sG || a.drop, SKP_STREAM, sm_count(), L.sk_flags + kMaxStreamK, 2,
                                1 << 1);
     if (cudaEventRecord(side.join, side.st) != cudaSuccess || cudaStreamWaitEvent(s, side.join, 0) != cudaSuccess)
         st = QLORA_ERR_CUDA;
@@ -938,7 +944,16 @@ inline qlora_status linear_bwd_impl(const void* dY, const void* X, const LinearA
         }
         return QLORA_OK;
     }
-    if (dX &&
+    SideStream side{nullptr, nullptr, nullptr};
+    const bool forked = dX && a.r > 0 && side_fork_ok() && side_stream_acquire(s, &side);
+    struct Release {
+        bool on;
+        ~Release() {
+            if (on) side_stream_release();
+        }
+    } release{forked};
+    // (the forked order under dropout expands the block constants later)
+    if (dX && !(forked && a.drop && !a.have_sG) &&
         launch_expand_scales(w, L.scales, L.scales_ld, s, L.sk_flags, kMaxStreamK + 2, a.have_sG) != cudaSuccess)
         return QLORA_ERR_CUDA;
     if (a.have_sG) {
@@ -948,12 +963,7 @@ inline qlora_status linear_bwd_impl(const void* dY, const void* X, const LinearA
     }
     CUtensorMap tdY;
     if (!map_bf16(&tdY, dY, a.N, a.M, 128)) return QLORA_ERR_CUDA;
-    SideStream side{nullptr, nullptr, nullptr};
-    if (dX && a.r > 0 && side_fork_ok() && side_stream_acquire(s, &side)) {
-        const qlora_status st = linear_bwd_forked(dY, X, a, A, B, dX, dA, dB, L, tdY, side, s);
-        side_stream_release();
-        return st;
-    }
+    if (forked) return linear_bwd_forked(dY, X, a, A, B, dX, dA, dB, L, tdY, side, s);
     // serial path: sU and sG in one launch, dX GEMM, dA and dB
     if (a.r > 0) {
         SkinnyDesc d[2];
