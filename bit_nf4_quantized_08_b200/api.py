@@ -320,6 +320,12 @@ def _adapter_rank(X: torch.Tensor, w: NF4Weight, nseg: int, A: torch.Tensor | No
     return X.shape[0], r
 
 
+def _step_workspace(nbytes: int, device, ws: torch.Tensor | None) -> torch.Tensor:
+    if ws is not None and (ws.device != device or not ws.is_contiguous()):
+        raise ValueError(f"ws must be contiguous on {device}")
+    return _workspace(nbytes, device, ws)
+
+
 def _adapter_grads(dA, dB, rows_a: int, w: NF4Weight, r: int, grad_dtype, device):
     if grad_dtype not in _GRAD_DTYPES:
         raise TypeError("grad_dtype must be torch.float32 or torch.bfloat16")
@@ -364,7 +370,7 @@ def qlora_fused_linear_dropout_fwd(X: torch.Tensor, w: NF4Weight, nseg: int, A: 
     if Y is None:
         Y = torch.empty(M, w.rows, dtype=torch.bfloat16, device=X.device)
     _expect(Y, "Y", (M, w.rows), torch.bfloat16, X.device)
-    wsb = _workspace(qlora_fused_linear_dropout_workspace(M, w, nseg, r, False), X.device, ws)
+    wsb = _step_workspace(qlora_fused_linear_dropout_workspace(M, w, nseg, r, False), X.device, ws)
     cw = w.c_struct()
     with _on(X.device):
         check(lib().qlora_fused_linear_dropout_fwd(_ptr(X), M, ctypes.byref(cw), nseg, _ptr(A), _ptr(B), r,
@@ -387,7 +393,7 @@ def qlora_fused_linear_dropout_bwd(dY: torch.Tensor, X: torch.Tensor, w: NF4Weig
         dX = torch.empty(M, w.cols, dtype=torch.bfloat16, device=X.device)
     _expect(dX, "dX", (M, w.cols), torch.bfloat16, X.device, optional=not want_dx)
     dA, dB = _adapter_grads(dA, dB, nseg * r, w, r, grad_dtype, X.device)
-    wsb = _workspace(qlora_fused_linear_dropout_workspace(M, w, nseg, r, True), X.device, ws)
+    wsb = _step_workspace(qlora_fused_linear_dropout_workspace(M, w, nseg, r, True), X.device, ws)
     cw = w.c_struct()
     with _on(X.device):
         check(lib().qlora_fused_linear_dropout_bwd(
@@ -423,7 +429,7 @@ def qlora_gated_linear_fwd(X: torch.Tensor, w: NF4Weight, A: torch.Tensor | None
         GU = torch.empty(M, w.rows, dtype=torch.bfloat16, device=X.device)
     _expect(H, "H", (M, F), torch.bfloat16, X.device)
     _expect(GU, "GU", (M, w.rows), torch.bfloat16, X.device, optional=True)
-    wsb = _workspace(qlora_gated_linear_workspace(M, w, r, False), X.device, ws)
+    wsb = _step_workspace(qlora_gated_linear_workspace(M, w, r, False), X.device, ws)
     cw = w.c_struct()
     with _on(X.device):
         check(lib().qlora_gated_linear_fwd(_ptr(X), M, ctypes.byref(cw), _ptr(A), _ptr(B), r, float(scale), _act(act),
@@ -447,7 +453,7 @@ def qlora_gated_linear_bwd(dH: torch.Tensor, X: torch.Tensor, GU: torch.Tensor, 
         dX = torch.empty(M, w.cols, dtype=torch.bfloat16, device=X.device)
     _expect(dX, "dX", (M, w.cols), torch.bfloat16, X.device, optional=not want_dx)
     dA, dB = _adapter_grads(dA, dB, 2 * r, w, r, grad_dtype, X.device)
-    wsb = _workspace(qlora_gated_linear_workspace(M, w, r, True), X.device, ws)
+    wsb = _step_workspace(qlora_gated_linear_workspace(M, w, r, True), X.device, ws)
     cw = w.c_struct()
     with _on(X.device):
         check(lib().qlora_gated_linear_bwd(

@@ -10,9 +10,10 @@
 // 128 x 256 x 16 products (about 0.28 us) consumes 16384 weights.  (With the
 // weight rows on the 128-row M side, as in the plain small-M linear, the same
 // four issues and two commits consume 8192 in about 0.45 us, whatever the
-// token count: the issue cost of small products bounds that form.)  The token
-// tile's unused rows hold whatever follows it in shared memory; they only
-// reach accumulator rows that nobody reads.
+// token count: the issue cost of small products bounds that form; projection
+// and activation apart took 186 us on LLaMA-65B at 48 tokens, this 147 us.)
+// The token tile's unused rows hold whatever follows it in shared memory; they
+// only reach accumulator rows that nobody reads.
 //
 // The units, tiles x KS with KS = K/64 + ceil(2r/64), are split evenly over a
 // persistent grid of one CTA per SM (stream-K).  A tile's g and u sit in one
@@ -23,8 +24,17 @@
 //
 // Roles: warp 0 loads the codes and warp 6 the token tiles (X or sU) with TMA,
 // warp 1 issues the MMAs, warps 2-5 drain the accumulators (double-buffered in
-// TMEM), and two groups of eight dequant warps expand alternate units, one thread per weight row, the
-// block constants straight from the 8-bit codes.
+// TMEM), and three groups of eight dequant warps expand the units in turn, one
+// thread per weight row, the block constants straight from the 8-bit codes.
+// Warp 7 is idle: the groups start on a multiple of the four schedulers.
+//
+// Bound by the expansion (its integer pipe is busy for 64 % of the time) and
+// the hand-overs between loads, expansion and products, not by HBM: codes and
+// constants are 46 MB on LLaMA-7B (7 us) and 186 MB on LLaMA-65B (28 us).
+// Measured with cold caches, kernel alone: LLaMA-65B 133 us at 48 tokens (1.4
+// TB/s), LLaMA-7B 44 us at one (1.1 TB/s).  With two groups instead of three
+// 65B took 151 us; two block columns a slot, 128-byte code lines, or a table of
+// code pairs in shared memory instead of the byte permutes were no faster.
 #pragma once
 
 #include "common.cuh"
@@ -357,25 +367,25 @@ __global__ void __launch_bounds__(GatedSmallShape<TOK>::THREADS, 1)
             __threadfence();
             named_bar(1, 128);
             if (et == 0) {
+                // (also after an abort, so that the count starts at 0 again
+                // when a captured launch is replayed)
                 int last = 0;
-                if (!*abort_flag) {
-                    unsigned long long* ctr = p.counters + tile;
-                    unsigned long long cv = *reinterpret_cast<volatile unsigned long long*>(ctr);
-                    const unsigned long long ep = (unsigned long long)p.epoch << 32;
-                    while (true) {
-                        // a value of another epoch counts as no arrivals
-                        const bool same = (cv & 0xFFFFFFFF00000000ull) == ep;
-                        const unsigned long long want = same ? cv + 1ull : (ep | 1ull);
-                        const unsigned long long prev = atomicCAS(ctr, cv, want);
-                        if (prev == cv) {
-                            last = (int)(want & 0xFFFFFFFFull) == cl - cf + 1;
-                            break;
-                        }
-                        cv = prev;
+                unsigned long long* ctr = p.counters + tile;
+                unsigned long long cv = *reinterpret_cast<volatile unsigned long long*>(ctr);
+                const unsigned long long ep = (unsigned long long)p.epoch << 32;
+                while (true) {
+                    // a value of another epoch counts as no arrivals
+                    const bool same = (cv & 0xFFFFFFFF00000000ull) == ep;
+                    const unsigned long long want = same ? cv + 1ull : (ep | 1ull);
+                    const unsigned long long prev = atomicCAS(ctr, cv, want);
+                    if (prev == cv) {
+                        last = (int)(want & 0xFFFFFFFFull) == cl - cf + 1;
+                        break;
                     }
-                    if (last) *ctr = 0ull;  // for a replay of this launch
+                    cv = prev;
                 }
-                *last_flag = last;
+                if (last) *ctr = 0ull;  // for a replay of this launch
+                *last_flag = last && !*abort_flag;
             }
             named_bar(1, 128);
             const bool last = *last_flag != 0;

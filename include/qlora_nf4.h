@@ -500,6 +500,9 @@ void qlora_set_wait_timeout_ns(uint64_t ns);
  * meant for tests only.  Likewise the environment variable QLORA_SCHEDULE
  * (pair | pairsk | grid | streamk: the schedule of the large-M GEMMs) is read
  * once, at the first large-M call of the process, and applies to all calls.
+ * The gated forward and the dX GEMM under adapter dropout have one kernel each
+ * (per token class) and one schedule: modes 2 to 4, 7 and 8 and QLORA_SCHEDULE
+ * leave them as they are.
  */
 void qlora_debug_inject(int32_t mode);
 
@@ -519,10 +522,11 @@ void qlora_debug_inject(int32_t mode);
 typedef enum {
     QLORA_KERNEL_QUANTIZE = 0,  /* blockwise NF4 quantizer (first kernel of qlora_nf4_quantize) */
     QLORA_KERNEL_DEQUANTIZE = 1,
-    QLORA_KERNEL_FWD_GEMM = 2,  /* forward dequant-GEMM, M > 64 */
+    QLORA_KERNEL_FWD_GEMM = 2,  /* forward dequant-GEMM, M > 64 (gated: M > 128) */
     QLORA_KERNEL_DX_GEMM = 3,   /* backward dX dequant-GEMM */
-    QLORA_KERNEL_SMALLM_GEMM = 4, /* forward dequant-GEMM, M <= 64 */
-    QLORA_KERNEL_LORA_GEMM = 5, /* rank-r LoRA GEMMs (U, G, dA, dB) */
+    QLORA_KERNEL_SMALLM_GEMM = 4, /* forward dequant-GEMM, M <= 64 (gated: M <= 128) */
+    QLORA_KERNEL_LORA_GEMM = 5, /* rank-r LoRA GEMMs (U, G, dA, dB), except G where the gated
+                                   backward's first pass forms it */
     QLORA_KERNEL_MERGE = 6,     /* LoRA merge / unmerge */
     QLORA_KERNEL_KINDS = 7
 } qlora_kernel_kind;

@@ -360,3 +360,66 @@ def test_waits_run_out_and_recover(Q, cuda):
         got = calls(*a)
         assert Q.qlora_get_last_error() == 0
         assert all(_same_bits(x, y) for x, y in zip(got, r))
+
+
+def test_workspace_of_another_place_is_refused(Q, cuda):
+    """A workspace on another device, or with gaps, would be written out of its bounds."""
+    q, inp, _ = _setup(Q, 8, 256, 128, 8, seed=19)
+    t = _dev(inp)
+    n = Q.qlora_gated_linear_workspace(8, q, 8, True) + Q.qlora_gated_linear_workspace(8, q, 8, False)
+    bad = [torch.empty(n, dtype=torch.uint8), torch.empty(2 * n, dtype=torch.uint8, device=cuda)[::2]]
+    dY = torch.zeros(8, 512, dtype=torch.bfloat16, device=cuda)
+    for ws in bad:
+        for call in (lambda: Q.qlora_gated_linear_fwd(t["X"], q, t["A"], t["B"], 1.0, ws=ws),
+                     lambda: Q.qlora_gated_linear_bwd(t["dH"], t["X"], dY, q, t["A"], t["B"], 1.0, ws=ws),
+                     lambda: Q.qlora_fused_linear_dropout_fwd(t["X"], q, 2, t["A"], t["B"], 1.0, None, ws=ws),
+                     lambda: Q.qlora_fused_linear_dropout_bwd(dY, t["X"], q, 2, t["A"], t["B"], 1.0, None, ws=ws)):
+            with pytest.raises(ValueError, match="ws must be"):
+                call()
+
+
+def test_gated_calls_on_several_streams_at_once(Q, cuda):
+    """Forward and backward of three token classes on a stream each, with a workspace each: the bits of calls alone."""
+    sets = []
+    for M in (7, 100, 400):
+        q, inp, _ = _setup(Q, M, 1024, 512, 16, seed=30 + M)
+        sets.append((q, _dev(inp), Q.Dropout(0.2, M, 1)))
+
+    def calls(q, t, d):
+        H, GU = Q.qlora_gated_linear_fwd(t["X"], q, t["A"], t["B"], 2.0, "silu", d, want_gu=True)
+        return (H, GU, *Q.qlora_gated_linear_bwd(t["dH"], t["X"], GU, q, t["A"], t["B"], 2.0, "silu", d))
+
+    ref = [calls(*a) for a in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = []
+    for _ in range(5):
+        for a, s in zip(sets, streams):
+            with torch.cuda.stream(s):
+                got.append(calls(*a))
+    torch.cuda.synchronize()
+    assert Q.qlora_get_last_error() == 0
+    for i, g in enumerate(got):
+        assert all(_same_bits(a, b) for a, b in zip(g, ref[i % len(sets)]))
+
+
+@pytest.mark.parametrize("M", [9, 48, 200])
+def test_gated_token_of_nan_stays_in_its_row(Q, cuda, M):
+    """A token of NaN (an unused slot of a padded batch) changes no other token's H, GU or dX."""
+    q, inp, _ = _setup(Q, M, 512, 320, 16, seed=33)
+    t = _dev(inp)
+    bad = M // 2
+    rows = torch.arange(M, device=cuda) != bad
+    X2, dH2 = t["X"].clone(), t["dH"].clone()
+    X2[bad] = float("nan")
+    dH2[bad] = float("nan")
+    d = Q.Dropout(0.2, 3, 1)
+    outs = []
+    for X, dH in ((t["X"], t["dH"]), (X2, dH2)):
+        H, GU = Q.qlora_gated_linear_fwd(X, q, t["A"], t["B"], 2.0, "silu", d, want_gu=True)
+        dX, _, _ = Q.qlora_gated_linear_bwd(dH, X, GU, q, t["A"], t["B"], 2.0, "silu", d)
+        outs.append((H, GU, dX))
+    torch.cuda.synchronize()
+    assert Q.qlora_get_last_error() == 0
+    for a, b in zip(*outs):
+        assert _same_bits(a[rows], b[rows]) and torch.isnan(b[bad]).all()
