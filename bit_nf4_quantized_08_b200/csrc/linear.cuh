@@ -22,6 +22,7 @@
 
 #include "dropout.cuh"
 #include "gated.cuh"
+#include "gated_few.cuh"
 #include "gated_small.cuh"
 #include "gemm.cuh"
 #include "gemm_pair.cuh"
@@ -999,6 +1000,8 @@ inline qlora_status linear_bwd_impl(const void* dY, const void* X, const LinearA
 // with cold caches: LLaMA-7B 128 / 129 tokens 113 / 111 us, LLaMA-65B 186 /
 // 285 us; at 16 tokens 7B 50 us, 65B 133 us.
 constexpr int kGatedSmall = 128;
+// Most tokens of k_gated_few.
+constexpr int kGatedFew = 16;
 
 struct BlockWs {
     void* linear;
@@ -1065,6 +1068,51 @@ inline qlora_status launch_sU(const void* X, const LinearArgs& a, const void* A,
     SkinnyDesc d;
     if (!desc_sU(&d, X, a, A, sU)) return QLORA_ERR_CUDA;
     return skinny(&d, 1, a.rt(), s, 1);
+}
+
+template <int NT>
+inline cudaError_t launch_gated_few_kernel(const GatedFewParams& p, int grid, cudaStream_t s) {
+    using S = GatedFewShape<NT>;
+    auto kern = k_gated_few<NT>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    if (e != cudaSuccess) return e;
+    ProfileScope ps(QLORA_KERNEL_SMALLM_GEMM, s);
+    note_launch();
+    return launch_pdl(kern, dim3((unsigned)grid, 1, 1), dim3(S::THREADS, 1, 1), S::SMEM, s, 0, p);
+}
+
+// H = act(g) u for M <= kGatedFew: a range of hidden columns per SM.
+inline qlora_status gated_fwd_few(const void* X, const LinearArgs& a, const void* A, const void* B, int act, void* H,
+                                  void* GU, const BlockWs& b, cudaStream_t s) {
+    const qlora_nf4_weight& w = *a.w;
+    if (a.r > 0) {
+        const qlora_status st = a.drop ? launch_sU(X, a, A, b.sU, s) : launch_small_u(X, a, A, b.sU, s);
+        if (st != QLORA_OK) return st;
+    }
+    GatedFewParams p;
+    memset(&p, 0, sizeof(p));
+    p.codes = w.codes;
+    p.X = static_cast<const uint16_t*>(X);
+    p.B = static_cast<const uint16_t*>(B);
+    p.sU = b.sU;
+    p.q8 = w.absmax_q8;
+    p.c1 = w.absmax_scale;
+    p.offset = w.absmax_offset;
+    p.absmax = w.absmax;
+    p.dq = w.double_quant;
+    p.fmt = weight_format(w);
+    p.F = (int)a.seg_rows;
+    p.M = (int)a.M;
+    p.K = (int)a.K;
+    p.kbs = (int)(a.K / 64);
+    p.r = a.r;
+    p.act = act;
+    p.inv_scale = 1.0f / (w.code_type ? 1.5f : 1.18881f);
+    p.H = static_cast<uint16_t*>(H);
+    p.GU = static_cast<uint16_t*>(GU);
+    const int grid = (int)std::min<int64_t>(std::min(sm_count(), kSms), a.seg_rows / 8);
+    const cudaError_t e = a.M <= 8 ? launch_gated_few_kernel<1>(p, grid, s) : launch_gated_few_kernel<2>(p, grid, s);
+    return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
 // H = act(g) u for M <= kGatedSmall on a persistent stream-K grid (one CTA per
@@ -1165,6 +1213,7 @@ inline qlora_status gated_fwd_large(const void* X, const LinearArgs& a, const vo
 inline qlora_status gated_fwd_impl(const void* X, const LinearArgs& a, const void* A, const void* B, int act,
                                    void* H, void* GU, void* ws, cudaStream_t s) {
     const BlockWs b = carve_block_ws(ws, a.M, a.N, a.K, a.rt(), 0);
+    if (a.M <= kGatedFew) return gated_fwd_few(X, a, A, B, act, H, GU, b, s);
     if (a.M <= kGatedSmall) return gated_fwd_small(X, a, A, B, act, H, GU, b, s);
     return gated_fwd_large(X, a, A, B, act, H, GU, b, s);
 }
