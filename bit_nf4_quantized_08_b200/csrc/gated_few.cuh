@@ -13,11 +13,18 @@
 // and forms H, and the tokens are the 8-column operand.
 //
 // A unit is (8 hidden columns, 256 elements of k): 16 lines of 128 bytes of
-// codes, which every lane loads straight into registers, two units ahead (64
-// KB in flight an SM); X comes through L1.  There is no ring, no barrier in the
-// loop and no warp that only moves data.  A CTA owns a range of hidden columns; its 16 warps
-// take the units in turn and leave fp32 partial sums in shared memory, which
-// are added in k order; then the adapters' products and the activation.
+// codes.  A CTA owns a range of hidden columns and each of its 16 warps some
+// unit columns (256 elements of k) of all of them, so that a warp's part of X
+// stays in registers.  Every warp has a ring of its own, filled by TMA two
+// units ahead (64 KB in flight an SM), and nothing in the loop waits for
+// another warp.  The warps' fp32 sums of a chunk of hidden columns pass through
+// shared memory and are added in warp order; then the adapters' products and
+// the activation.
+//
+// Within a block, lane position t of a fragment's group of four holds bytes
+// 4 t .. 4 t + 3 of both halves of a row's 32 code bytes (elements 8 t .. 8 t + 7
+// and 32 + 8 t .. + 7): a load of one word a lane then covers a 16-byte chunk of
+// eight rows, which the 128-byte swizzle spreads over all banks.
 #pragma once
 
 #include "common.cuh"
@@ -28,7 +35,8 @@
 namespace qlora {
 
 struct GatedFewParams {
-    const uint8_t* codes;  // [2F][K/2]
+    CUtensorMap tmCodes;   // codes [2F][K/2] bytes, box {128 B, 8 rows}, 128-byte swizzle
+    const uint8_t* codes;  // the same array
     const uint16_t* X;     // [M][K]
     const uint16_t* B;     // [2F][r]
     const uint16_t* sU;    // [M][2r]
@@ -43,6 +51,8 @@ struct GatedFewParams {
     QFormat fmt;
     uint16_t* H;           // [M][F]
     uint16_t* GU;          // [M][2F] or nullptr
+    uint64_t timeout_ns;
+    int inject;
 };
 
 // NT: token tiles of 8.
@@ -50,187 +60,304 @@ template <int NT>
 struct GatedFewShape {
     static constexpr int WARPS = 16;
     static constexpr int THREADS = 32 * WARPS;
-    static constexpr int CHUNK = NT == 1 ? 10 : 6;             // items (8 hidden columns) between two reductions
-    static constexpr int SMEM = CHUNK * WARPS * NT * 32 * 16;  // partial sums
+    static constexpr int STAGES = 3;                 // of a warp's ring
+    static constexpr int STAGE = 2048;               // 8 gate and 8 up rows of 128 bytes
+    static constexpr int CHUNK = NT == 1 ? 7 : 3;    // items (8 hidden columns) between two reductions
+    static constexpr int LUT_BYTES = 256 * 256;      // entry e of lane l at 256 e + 4 l
+    static constexpr int RING_BYTES = WARPS * STAGES * STAGE;
+    static constexpr int PART_BYTES = CHUNK * (WARPS + 1) * NT * 32 * 16;  // [item of the chunk][warp or remainder][NT][lane]
+    // partial sums up to address 65536, the table, the rings (a window's first 1 KB is the system's)
+    static constexpr int SMEM = 65536 + LUT_BYTES + RING_BYTES - 1024;
+    static_assert(SMEM + 1536 <= 232448 && PART_BYTES + 4096 <= 65536, "shared memory per CTA");
 };
+
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+// The pair of bf16 table values of byte k of w.  The table starts at a multiple
+// of 64 KB, which tl (this lane's column of the first entry) holds in its upper
+// half: one byte permute forms the address.
+__device__ __forceinline__ uint32_t few_pair(uint32_t w, int k, uint32_t tl) {
+    uint32_t v;
+    asm("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(prmt(w, tl, 0x7604u | (uint32_t)(k << 4))));
+    return v;
+}
 
 template <int NT>
 __global__ void __launch_bounds__(GatedFewShape<NT>::THREADS, 1) k_gated_few(const __grid_constant__ GatedFewParams p) {
     using S = GatedFewShape<NT>;
     constexpr int W = S::WARPS;
-    extern __shared__ __align__(16) uint8_t few_smem[];
-    float4* part = reinterpret_cast<float4*>(few_smem);  // [item of the chunk][warp][NT][lane]
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    const uint32_t dyn = smem_u32(smem_raw);
+    const uint32_t lut = (dyn + (uint32_t)S::PART_BYTES + 65535u) & ~65535u, base = lut + (uint32_t)S::LUT_BYTES;
+    float4* part = reinterpret_cast<float4*>(smem_raw);
     __shared__ float t8s[256];
+    __shared__ __align__(8) uint64_t full_bar[W * S::STAGES];
+    __shared__ volatile int abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
-    const uint32_t lane4 = (uint32_t)lane * 4u;
+    const uint32_t tl = lut + (uint32_t)lane * 4u;
     const int items = p.F / 8;
     const int i_begin = (int)((int64_t)items * blockIdx.x / gridDim.x);
     const int i_end = (int)((int64_t)items * (blockIdx.x + 1) / gridDim.x);
-    const int Q = (p.kbs + 3) >> 2;
-    const int d_it = W / Q, d_q = W % Q;
-    const int64_t ldc = p.K / 2;
+    const int Q = p.kbs >> 2, rem = p.kbs & 3;  // whole units of an item, and the block columns after them
+    const int NG = Q > 0 && Q < W ? W / Q : 1;  // warps on the same unit column take every NG-th item
+    const int e0 = Q < W && Q > 0 ? warp / Q : 0, q0 = Q < W && Q > 0 ? warp % Q : warp;
+    const bool busy = Q > 0 && e0 < NG;
+    const int64_t ldc = p.K / 2, up_c = (int64_t)p.F * ldc;
     const int sh = p.fmt.bs_shift;
+    const WaitCfg wc{p.timeout_ns};
+    const uint32_t full0 = smem_u32(full_bar) + 8u * (uint32_t)(warp * S::STAGES);
+    const uint32_t ring = base + (uint32_t)(warp * S::STAGES * S::STAGE);
 
     pdl_trigger();
+    if (lane == 0) {  // (the warp's own barriers)
+        for (int i = 0; i < S::STAGES; ++i) mbar_init(full0 + 8u * i, 1);
+        fence_mbar_init();
+        prefetch_tensormap(&p.tmCodes);
+    }
+    if (threadIdx.x == 0) abort_flag = 0;
+    __syncwarp();
     // With adapters the kernel before is the one that forms sU, which waited
     // for its own predecessors before it let this one start.
     if (p.r == 0) pdl_wait();
 
-    // A unit's codes (bytes 8 tig .. 8 tig + 7 of four 32-byte blocks, of a gate
-    // and an up row) and, for block column 4 q + tig, the raw block constants.
-    struct In {
-        uint2 c[4][2];
+    // Block constants: offsets from the group of 256 that holds the CTA's first
+    // gate (up) row's first block.  (At most 2^40 elements over the CTAs: they
+    // fit in 32 bits.)
+    struct Blocks {
+        const uint8_t* q8;
+        const float* f;  // c1 or absmax
+        uint32_t first;
+    };
+    auto blocks_at = [&](int64_t b) {
+        const int64_t b0 = b & ~(int64_t)1023;
+        return Blocks{p.dq ? p.q8 + (b0 >> sh) : nullptr, p.dq ? p.c1 + (b0 >> (sh + 8)) : p.absmax + (b0 >> sh),
+                      (uint32_t)(b - b0)};
+    };
+    const Blocks bg = blocks_at((int64_t)i_begin * 8 * p.kbs), bu = blocks_at(((int64_t)p.F + i_begin * 8) * p.kbs);
+    auto load_const = [&](const Blocks& t, uint32_t rel, float& sv, uint32_t& qv) {  // rel: blocks after the first
+        const uint32_t b = (t.first + rel) >> sh;
+        qv = p.dq ? (uint32_t)t.q8[b] : 0u;
+        sv = p.dq ? t.f[b >> 8] : t.f[b];
+    };
+    // The warp's units of a chunk: for each of its unit columns q, its items.
+    struct Pos {
+        int e, q;
+        uint32_t b;  // this lane's block of either row: column 4 q + tig
+    };
+    int item0 = i_begin, n_items = min(S::CHUNK, i_end - i_begin);
+    auto place = [&](Pos& u) {
+        u.b = (uint32_t)(((item0 - i_begin + u.e) * 8 + gid) * p.kbs + 4 * u.q + tig);
+    };
+    auto start = [&]() {
+        Pos u;
+        u.e = e0;
+        u.q = q0;
+        if (!busy || e0 >= n_items) u.q = Q;
+        place(u);
+        return u;
+    };
+    auto advance = [&](Pos& u) {
+        u.e += NG;
+        u.b += (uint32_t)(NG * 8 * p.kbs);
+        if (u.e >= n_items) {
+            u.e = e0;
+            u.q += W;
+            place(u);
+        }
+    };
+    // A unit's codes into ring stage st and, in registers, the raw constants of
+    // block column 4 q + tig of this lane's two rows.
+    struct Raw {
         float s[2];
         uint32_t q[2];
     };
-    auto fetch = [&](int it, int q, int n_items, int item0) {
-        In x;
-        const bool on = it < n_items;
-        const int64_t row = (int64_t)(item0 + it) * 8 + gid;
-        const uint8_t* cg = p.codes + row * ldc + q * 128 + tig * 8;
-        const uint8_t* cu = cg + (int64_t)p.F * ldc;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bool ok = on && 4 * q + i < p.kbs;
-            x.c[i][0] = ok ? __ldcs(reinterpret_cast<const uint2*>(cg + 32 * i)) : make_uint2(0u, 0u);
-            x.c[i][1] = ok ? __ldcs(reinterpret_cast<const uint2*>(cu + 32 * i)) : make_uint2(0u, 0u);
+    auto fetch = [&](Raw& x, int st, Pos& u) {
+        if (u.q >= Q) return;
+        if (lane == 0 && !p.inject) {
+            const uint32_t dst = ring + (uint32_t)(st * S::STAGE), bar = full0 + 8u * st;
+            const int row = (item0 + u.e) * 8;
+            mbar_arrive_expect_tx(bar, S::STAGE);
+            tma_load_2d(dst, &p.tmCodes, bar, u.q * 128, row);
+            tma_load_2d(dst + S::STAGE / 2, &p.tmCodes, bar, u.q * 128, p.F + row);
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t b = ((row + (int64_t)h * p.F) * p.kbs + 4 * q + tig) >> sh;
-            const bool ok = on && 4 * q + tig < p.kbs;
-            x.q[h] = ok && p.dq ? (uint32_t)p.q8[b] : 0u;
-            x.s[h] = ok ? (p.dq ? p.c1[b >> 8] : p.absmax[b]) : 0.0f;
-        }
-        return x;
+        load_const(bg, u.b, x.s[0], x.q[0]);
+        load_const(bu, u.b, x.s[1], x.q[1]);
+        advance(u);
     };
 
-    int item0 = i_begin, n_items = min(S::CHUNK, i_end - i_begin);
-    const int it_w = warp / Q, q_w = warp - it_w * Q;  // the warp's first unit of a chunk
-    In a = fetch(it_w, q_w, n_items, item0);
+    Raw raw[S::STAGES];
+    uint32_t phases = 0;   // parity of each stage's next use
+    bool dead = false;
+    Pos next = start();  // the next unit to load
+#pragma unroll
+    for (int i = 0; i < S::STAGES - 1; ++i) fetch(raw[i], i, next);
 
     // the table and the 8-bit code book, while the first loads are on their way
     {
         const float L = small_m_table_scale(p.fmt.code_type);
-        for (int idx = threadIdx.x; idx < 256 * 32; idx += S::THREADS) {
-            const int e = idx >> 5;
-            g_small_m_lut[idx] = pack_bf16x2(__fmul_rn(code_value(p.fmt.code_type, e >> 4), L),
-                                             __fmul_rn(code_value(p.fmt.code_type, e & 15), L));
-        }
+        for (int e = warp; e < 256; e += W)
+            *reinterpret_cast<uint32_t*>(smem_raw + (tl - dyn) + 256 * e) =
+                pack_bf16x2(__fmul_rn(code_value(p.fmt.code_type, e >> 4), L),
+                            __fmul_rn(code_value(p.fmt.code_type, e & 15), L));
     }
     for (int i = threadIdx.x; i < 256; i += S::THREADS)
         t8s[i] = dq_value(p.fmt.dq_type, (p.fmt.dq_type == 0 || i < 253) ? i : 0);
     const float off = p.dq ? *p.offset : 0.0f;
     __syncthreads();
 
-    for (; item0 < i_end; item0 += S::CHUNK) {
-        n_items = min(S::CHUNK, i_end - item0);
-        if (item0 != i_begin) a = fetch(it_w, q_w, n_items, item0);
-        float acc[NT][4];
+    auto load_x = [&](uint4 (&x)[NT][2], int kb) {  // (rows past the last token repeat it: nobody reads their sums)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n) {
+            const uint4* src =
+                reinterpret_cast<const uint4*>(p.X + (int64_t)min(8 * n + gid, p.M - 1) * p.K + kb * 64 + tig * 8);
+            x[n][0] = src[0];
+            x[n][1] = src[4];
+        }
+    };
+    auto block_const = [&](float s, uint32_t q) {
+        return (p.dq ? __fadd_rn(__fmul_rn(t8s[q], s), off) : s) * p.inv_scale;
+    };
+    // acc += the products of one block column
+    auto block = [&](float (&acc)[NT][4], const uint2& cg, const uint2& cu, const uint4 (&x)[NT][2], float sg, float su) {
+        float d[NT][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[n][e] = 0.0f;
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t wg = j < 2 ? cg.x : cg.y, wu = j < 2 ? cu.x : cu.y;
+            const int k = 2 * (j & 1);
+            const uint32_t a0 = few_pair(wg, k, tl), a1 = few_pair(wu, k, tl);
+            const uint32_t a2 = few_pair(wg, k + 1, tl), a3 = few_pair(wu, k + 1, tl);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const uint4 v = x[n][j >> 1];
+                const uint32_t b0 = j & 1 ? v.z : v.x, b1 = j & 1 ? v.w : v.y;
+                if (j == 0)
+                    mma_16816_z(d[n], a0, a1, a2, a3, b0, b1);
+                else
+                    mma_16816(d[n], a0, a1, a2, a3, b0, b1);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            acc[n][0] = __fmaf_rn(sg, d[n][0], acc[n][0]);
+            acc[n][1] = __fmaf_rn(sg, d[n][1], acc[n][1]);
+            acc[n][2] = __fmaf_rn(su, d[n][2], acc[n][2]);
+            acc[n][3] = __fmaf_rn(su, d[n][3], acc[n][3]);
+        }
+    };
 
-        auto consume = [&](const In& x, int q) {
-            float sc[2];
+    while (true) {
+        Pos u = start();
+        int xq = -1;
+        uint4 x[4][NT][2];
+        auto step = [&](const Raw& v, int st) {
+            if (u.q != xq) {
+                xq = u.q;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                sc[h] = (p.dq ? __fadd_rn(__fmul_rn(t8s[x.q[h]], x.s[h]), off) : x.s[h]) * p.inv_scale;
+                for (int i = 0; i < 4; ++i) load_x(x[i], 4 * xq + i);
+            }
+            const float sc0 = block_const(v.s[0], v.q[0]), sc1 = block_const(v.s[1], v.q[1]);
+            float acc[NT][4];
+            float4* slot = part + ((u.e * (W + 1) + warp) * NT) * 32 + lane;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float4 o = u.q >= W ? slot[n * 32] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                acc[n][0] = o.x;
+                acc[n][1] = o.y;
+                acc[n][2] = o.z;
+                acc[n][3] = o.w;
+            }
+            const uint32_t row = ring + (uint32_t)(st * S::STAGE) + (uint32_t)(gid * 128 + tig * 4) + ((uint32_t)gid << 4);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if (4 * q + i >= p.kbs) break;
-                float d[NT][4];
-                const float sg = __shfl_sync(0xffffffffu, sc[0], (lane & 28) | i);
-                const float su = __shfl_sync(0xffffffffu, sc[1], (lane & 28) | i);
-                uint4 xv[NT][2];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const int tok = 8 * n + gid;
-                    const uint4* src =
-                        reinterpret_cast<const uint4*>(p.X + (int64_t)tok * p.K + (4 * q + i) * 64 + tig * 16);
-                    xv[n][0] = tok < p.M ? src[0] : make_uint4(0u, 0u, 0u, 0u);
-                    xv[n][1] = tok < p.M ? src[1] : make_uint4(0u, 0u, 0u, 0u);
-                }
-                const uint32_t wg[2] = {x.c[i][0].x, x.c[i][0].y}, wu[2] = {x.c[i][1].x, x.c[i][1].y};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int k = 2 * (j & 1);
-                    const uint32_t a0 = lut_byte(wg[j >> 1], k, lane4), a1 = lut_byte(wu[j >> 1], k, lane4);
-                    const uint32_t a2 = lut_byte(wg[j >> 1], k + 1, lane4), a3 = lut_byte(wu[j >> 1], k + 1, lane4);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const uint4 v = xv[n][j >> 1];
-                        const uint32_t b0 = j & 1 ? v.z : v.x, b1 = j & 1 ? v.w : v.y;
-                        if (j == 0)
-                            mma_16816_z(d[n], a0, a1, a2, a3, b0, b1);
-                        else
-                            mma_16816(d[n], a0, a1, a2, a3, b0, b1);
-                    }
-                }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    acc[n][0] = __fmaf_rn(sg, d[n][0], acc[n][0]);
-                    acc[n][1] = __fmaf_rn(sg, d[n][1], acc[n][1]);
-                    acc[n][2] = __fmaf_rn(su, d[n][2], acc[n][2]);
-                    acc[n][3] = __fmaf_rn(su, d[n][3], acc[n][3]);
-                }
+                const uint32_t c0 = row ^ (uint32_t)(i << 5), c1 = c0 ^ 16u;
+                block(acc, make_uint2(ld_shared_u32(c0), ld_shared_u32(c1)),
+                      make_uint2(ld_shared_u32(c0 + S::STAGE / 2), ld_shared_u32(c1 + S::STAGE / 2)), x[i],
+                      __shfl_sync(0xffffffffu, sc0, (lane & 28) | i), __shfl_sync(0xffffffffu, sc1, (lane & 28) | i));
             }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) slot[n * 32] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+            advance(u);
         };
-
-        int it = it_w, q = q_w;
-        int itn = it + d_it, qn = q + d_q;  // the unit after it
-        if (qn >= Q) { qn -= Q; ++itn; }
-        In b = fetch(itn, qn, n_items, item0);
-        while (it < n_items) {
-            int it2 = itn + d_it, q2 = qn + d_q;
-            if (q2 >= Q) { q2 -= Q; ++it2; }
-            const In c = fetch(it2, q2, n_items, item0);
-            consume(a, q);
-            if (itn != it) {  // the warp's last unit of this item
+        // (the stages take turns: the loop is unrolled by their number)
+        while (u.q < Q) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    part[((it * W + warp) * NT + n) * 32 + lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[n][e] = 0.0f;
+            for (int i = 0; i < S::STAGES; ++i) {
+                if (u.q >= Q) break;
+                // every lane is done with the unit before: its sums, which
+                // depend on all that it read, are stored
+                __syncwarp();
+                if (!dead) fetch(raw[(i + S::STAGES - 1) % S::STAGES], (i + S::STAGES - 1) % S::STAGES, next);
+                if (!dead && !__all_sync(0xffffffffu, mbar_wait(full0 + 8u * i, (phases >> i) & 1u, wc))) {
+                    dead = true;
+                    abort_flag = 1;
                 }
+                if (dead) {
+                    advance(u);
+                    continue;
+                }
+                phases ^= 1u << i;
+                step(raw[i], i);
             }
-            a = b;
-            b = c;
-            it = itn;
-            q = qn;
-            itn = it2;
-            qn = q2;
         }
+        // the block columns after the last whole unit
+        if (rem)
+            for (int e = warp; e < n_items; e += W) {
+                float acc[NT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[n][j] = 0.0f;
+                const int64_t row = (int64_t)(item0 + e) * 8 + gid;
+#pragma unroll 1
+                for (int kb = 4 * Q; kb < p.kbs; ++kb) {
+                    const uint8_t* c = p.codes + row * ldc + (int64_t)kb * 32 + tig * 4;
+                    float s0, s1;
+                    uint32_t v0, v1;
+                    const uint32_t b = (uint32_t)(((item0 - i_begin + e) * 8 + gid) * p.kbs + kb);
+                    load_const(bg, b, s0, v0);
+                    load_const(bu, b, s1, v1);
+                    uint4 xr[NT][2];
+                    load_x(xr, kb);
+                    auto word = [&](int64_t o) { return *reinterpret_cast<const uint32_t*>(c + o); };
+                    block(acc, make_uint2(word(0), word(16)), make_uint2(word(up_c), word(up_c + 16)), xr,
+                          block_const(s0, v0), block_const(s1, v1));
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    part[((e * (W + 1) + W) * NT + n) * 32 + lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+            }
         if (p.r > 0) pdl_wait();  // sU
         __syncthreads();
 
-        // an item a warp: the partial sums in the order of their first block
-        // column, then the adapters
+        // an item a warp: the warps' partial sums in order, then the adapters
         for (int e = warp; e < n_items; e += W) {
-            const int cnt = min(Q, W), w0 = (int)((int64_t)e * Q % W);
+            const int w0 = Q < W ? (e % NG) * Q : 0, cnt = min(Q, W);
             const int f = (item0 + e) * 8 + gid;
-            const int64_t fg = (int64_t)f * p.r, fu = (int64_t)(p.F + f) * p.r;
+            const int64_t fg = (int64_t)f * p.r, fu = ((int64_t)p.F + f) * p.r;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                for (int j = 0; j < cnt; ++j) {
-                    const float4 s = part[((e * W + (w0 + j) % W) * NT + n) * 32 + lane];
-                    v[0] = __fadd_rn(v[0], s.x);
-                    v[1] = __fadd_rn(v[1], s.y);
-                    v[2] = __fadd_rn(v[2], s.z);
-                    v[3] = __fadd_rn(v[3], s.w);
-                }
-                const int tok = 8 * n + gid;
-                const int64_t tu = (int64_t)tok * 2 * p.r;
+                auto add = [&](int w) {
+                    const float4 o = part[((e * (W + 1) + w) * NT + n) * 32 + lane];
+                    v[0] = __fadd_rn(v[0], o.x);
+                    v[1] = __fadd_rn(v[1], o.y);
+                    v[2] = __fadd_rn(v[2], o.z);
+                    v[3] = __fadd_rn(v[3], o.w);
+                };
+                for (int j = 0; j < cnt; ++j) add(w0 + j);
+                if (rem) add(W);
+                const int64_t tu = (int64_t)min(8 * n + gid, p.M - 1) * 2 * p.r;
                 for (int j0 = 0; j0 < p.r; j0 += 32) {
                     const int j = j0 + 8 * tig;
                     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-                    const bool on = j < p.r, ont = on && tok < p.M;
+                    const bool on = j < p.r;
                     const uint4 bg = on ? *reinterpret_cast<const uint4*>(p.B + fg + j) : z;
                     const uint4 bu = on ? *reinterpret_cast<const uint4*>(p.B + fu + j) : z;
-                    const uint4 ug = ont ? *reinterpret_cast<const uint4*>(p.sU + tu + j) : z;
-                    const uint4 uu = ont ? *reinterpret_cast<const uint4*>(p.sU + tu + p.r + j) : z;
+                    const uint4 ug = on ? *reinterpret_cast<const uint4*>(p.sU + tu + j) : z;
+                    const uint4 uu = on ? *reinterpret_cast<const uint4*>(p.sU + tu + p.r + j) : z;
                     mma_16816(v, bg.x, 0u, bg.y, 0u, ug.x, ug.y);
                     mma_16816(v, bg.z, 0u, bg.w, 0u, ug.z, ug.w);
                     mma_16816(v, 0u, bu.x, 0u, bu.y, uu.x, uu.y);
@@ -239,18 +366,31 @@ __global__ void __launch_bounds__(GatedFewShape<NT>::THREADS, 1) k_gated_few(con
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int m = 8 * n + 2 * tig + h;
-                    if (m >= p.M || !QLORA_CHECK(f < p.F)) continue;
-                    const float g = v[h], u = v[2 + h];
-                    const float y = (p.act == ACT_SILU ? act_value(ACT_SILU, g) : act_value(ACT_GELU_TANH, g)) * u;
+                    if (m >= p.M || abort_flag || !QLORA_CHECK(f < p.F)) continue;
+                    const float g = v[h], u1 = v[2 + h];
+                    const float y = (p.act == ACT_SILU ? act_value(ACT_SILU, g) : act_value(ACT_GELU_TANH, g)) * u1;
                     p.H[(int64_t)m * p.F + f] = (uint16_t)(pack_bf16x2(y, 0.0f) & 0xFFFFu);
                     if (p.GU) {
                         p.GU[(int64_t)m * 2 * p.F + f] = (uint16_t)(pack_bf16x2(g, 0.0f) & 0xFFFFu);
-                        p.GU[(int64_t)m * 2 * p.F + p.F + f] = (uint16_t)(pack_bf16x2(u, 0.0f) & 0xFFFFu);
+                        p.GU[(int64_t)m * 2 * p.F + p.F + f] = (uint16_t)(pack_bf16x2(u1, 0.0f) & 0xFFFFu);
                     }
                 }
             }
         }
-        if (item0 + S::CHUNK < i_end) __syncthreads();  // the partial sums are read
+        item0 += S::CHUNK;
+        if (item0 >= i_end) break;
+        n_items = min(S::CHUNK, i_end - item0);
+        next = start();
+        if (!dead) {
+#pragma unroll
+            for (int i = 0; i < S::STAGES - 1; ++i) fetch(raw[i], i, next);
+        }
+        __syncthreads();  // the partial sums are read
+    }
+    // (every load has landed: a unit that was fetched has been waited for,
+    // unless a wait ran out)
+    if (dead) {
+        for (int i = 0; i < S::STAGES; ++i) mbar_wait(full0 + 8u * i, (phases >> i) & 1u, wc);
     }
 }
 

@@ -1091,7 +1091,10 @@ inline qlora_status gated_fwd_few(const void* X, const LinearArgs& a, const void
     }
     GatedFewParams p;
     memset(&p, 0, sizeof(p));
+    if (!map_codes(&p.tmCodes, w, 128, 8)) return QLORA_ERR_CUDA;
     p.codes = w.codes;
+    p.timeout_ns = wait_timeout_ns();
+    p.inject = inject_mode() == 1 ? 1 : 0;
     p.X = static_cast<const uint16_t*>(X);
     p.B = static_cast<const uint16_t*>(B);
     p.sU = b.sU;
