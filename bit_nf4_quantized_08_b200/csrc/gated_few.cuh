@@ -1,4 +1,4 @@
-// gated_few.cuh -- the gated feed-forward's forward for the fewest tokens
+// gated_few.cuh -- the gated feed-forward's forward for up to 8 tokens
 // (decoding), where a weight is used so seldom that expanding it into a
 // tensor-core operand in shared memory costs more than the products.
 //
@@ -25,6 +25,15 @@
 // 4 t .. 4 t + 3 of both halves of a row's 32 code bytes (elements 8 t .. 8 t + 7
 // and 32 + 8 t .. + 7): a load of one word a lane then covers a 16-byte chunk of
 // eight rows, which the 128-byte swizzle spreads over all banks.
+//
+// Bound by shared memory: about 34 wavefronts for a 64-element block of 16 rows,
+// 16 of them table lookups, keep that pipe busy for 62 % of the time, and the
+// latencies of 16 warps a SM take most of the rest; HBM (28 us on LLaMA-65B, 7
+// us on LLaMA-7B) does not.  One token, cold caches, kernel alone: LLaMA-65B 75
+// us (2.5 TB/s), LLaMA-7B 25 us (1.8 TB/s; about 9 us of it are start, table,
+// adapters and end).  On LLaMA-65B it was 105 us with codes and constants
+// loaded straight into registers, X read per block and a two-instruction table
+// address, and 92 us with X kept in registers.
 #pragma once
 
 #include "common.cuh"
@@ -51,21 +60,20 @@ struct GatedFewParams {
     QFormat fmt;
     uint16_t* H;           // [M][F]
     uint16_t* GU;          // [M][2F] or nullptr
+    int late, less;        // CTAs that start late, and the items that they have fewer
     uint64_t timeout_ns;
     int inject;
 };
 
-// NT: token tiles of 8.
-template <int NT>
 struct GatedFewShape {
     static constexpr int WARPS = 16;
     static constexpr int THREADS = 32 * WARPS;
     static constexpr int STAGES = 3;                 // of a warp's ring
     static constexpr int STAGE = 2048;               // 8 gate and 8 up rows of 128 bytes
-    static constexpr int CHUNK = NT == 1 ? 7 : 3;    // items (8 hidden columns) between two reductions
+    static constexpr int CHUNK = 7;                  // most items (8 hidden columns) between two reductions
     static constexpr int LUT_BYTES = 256 * 256;      // entry e of lane l at 256 e + 4 l
     static constexpr int RING_BYTES = WARPS * STAGES * STAGE;
-    static constexpr int PART_BYTES = CHUNK * (WARPS + 1) * NT * 32 * 16;  // [item of the chunk][warp or remainder][NT][lane]
+    static constexpr int PART_BYTES = CHUNK * (WARPS + 1) * 32 * 16;  // [item of the chunk][warp or remainder][lane]
     // partial sums up to address 65536, the table, the rings (a window's first 1 KB is the system's)
     static constexpr int SMEM = 65536 + LUT_BYTES + RING_BYTES - 1024;
     static_assert(SMEM + 1536 <= 232448 && PART_BYTES + 4096 <= 65536, "shared memory per CTA");
@@ -85,9 +93,8 @@ __device__ __forceinline__ uint32_t few_pair(uint32_t w, int k, uint32_t tl) {
     return v;
 }
 
-template <int NT>
-__global__ void __launch_bounds__(GatedFewShape<NT>::THREADS, 1) k_gated_few(const __grid_constant__ GatedFewParams p) {
-    using S = GatedFewShape<NT>;
+__global__ void __launch_bounds__(GatedFewShape::THREADS, 1) k_gated_few(const __grid_constant__ GatedFewParams p) {
+    using S = GatedFewShape;
     constexpr int W = S::WARPS;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     const uint32_t dyn = smem_u32(smem_raw);
@@ -99,8 +106,17 @@ __global__ void __launch_bounds__(GatedFewShape<NT>::THREADS, 1) k_gated_few(con
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
     const uint32_t tl = lut + (uint32_t)lane * 4u;
     const int items = p.F / 8;
-    const int i_begin = (int)((int64_t)items * blockIdx.x / gridDim.x);
-    const int i_end = (int)((int64_t)items * (blockIdx.x + 1) / gridDim.x);
+    // The last `late` CTAs find their SM when the kernel that forms sU has left
+    // it, and take `less` items fewer than the others.
+    const int G = gridDim.x, n_max = (items + G - 1) / G;
+    const int less = min(p.less, n_max - 1), early = G - p.late;
+    auto first_item = [&](int b) {
+        const int64_t w = (int64_t)b * n_max - (int64_t)max(b - early, 0) * less;
+        return (int)(items * w / ((int64_t)G * n_max - (int64_t)p.late * less));
+    };
+    const int i_begin = first_item(blockIdx.x), i_end = first_item(blockIdx.x + 1);
+    const int chunks = (i_end - i_begin + S::CHUNK - 1) / S::CHUNK;
+    const int chunk = chunks > 0 ? (i_end - i_begin + chunks - 1) / chunks : 1;  // even parts
     const int Q = p.kbs >> 2, rem = p.kbs & 3;  // whole units of an item, and the block columns after them
     const int NG = Q > 0 && Q < W ? W / Q : 1;  // warps on the same unit column take every NG-th item
     const int e0 = Q < W && Q > 0 ? warp / Q : 0, q0 = Q < W && Q > 0 ? warp % Q : warp;
@@ -147,7 +163,7 @@ __global__ void __launch_bounds__(GatedFewShape<NT>::THREADS, 1) k_gated_few(con
         int e, q;
         uint32_t b;  // this lane's block of either row: column 4 q + tig
     };
-    int item0 = i_begin, n_items = min(S::CHUNK, i_end - i_begin);
+    int item0 = i_begin, n_items = min(chunk, i_end - i_begin);
     auto place = [&](Pos& u) {
         u.b = (uint32_t)(((item0 - i_begin + u.e) * 8 + gid) * p.kbs + 4 * u.q + tig);
     };
@@ -195,6 +211,29 @@ __global__ void __launch_bounds__(GatedFewShape<NT>::THREADS, 1) k_gated_few(con
 #pragma unroll
     for (int i = 0; i < S::STAGES - 1; ++i) fetch(raw[i], i, next);
 
+    // (token rows past the last repeat it: nobody reads their sums)
+    auto load_x = [&](uint4 (&x)[2], int kb) {
+        const uint4* src =
+            reinterpret_cast<const uint4*>(p.X + (int64_t)min(gid, p.M - 1) * p.K + kb * 64 + tig * 8);
+        x[0] = src[0];
+        x[1] = src[4];
+    };
+    uint4 x[4][2];
+    int xq = -1;  // the unit column whose X the warp holds
+    if (busy && i_end > i_begin) {
+        xq = q0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load_x(x[i], 4 * xq + i);
+    }
+    // the adapters' B rows of this CTA on their way to L2
+    if (p.r > 0) {
+        const int lines = (i_end - i_begin) * 8 * p.r * 2 / 128 + 1;
+        for (int i = threadIdx.x; i < 2 * lines; i += S::THREADS) {
+            const int64_t row = (int64_t)i_begin * 8 + (i >= lines ? p.F : 0);
+            const int64_t at = min(row * p.r + (int64_t)(i >= lines ? i - lines : i) * 64, (int64_t)2 * p.F * p.r - 1);
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.B + at));
+        }
+    }
     // the table and the 8-bit code book, while the first loads are on their way
     {
         const float L = small_m_table_scale(p.fmt.code_type);
@@ -208,50 +247,32 @@ __global__ void __launch_bounds__(GatedFewShape<NT>::THREADS, 1) k_gated_few(con
     const float off = p.dq ? *p.offset : 0.0f;
     __syncthreads();
 
-    auto load_x = [&](uint4 (&x)[NT][2], int kb) {  // (rows past the last token repeat it: nobody reads their sums)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const uint4* src =
-                reinterpret_cast<const uint4*>(p.X + (int64_t)min(8 * n + gid, p.M - 1) * p.K + kb * 64 + tig * 8);
-            x[n][0] = src[0];
-            x[n][1] = src[4];
-        }
-    };
     auto block_const = [&](float s, uint32_t q) {
         return (p.dq ? __fadd_rn(__fmul_rn(t8s[q], s), off) : s) * p.inv_scale;
     };
     // acc += the products of one block column
-    auto block = [&](float (&acc)[NT][4], const uint2& cg, const uint2& cu, const uint4 (&x)[NT][2], float sg, float su) {
-        float d[NT][4];
+    auto block = [&](float (&acc)[4], const uint2& cg, const uint2& cu, const uint4 (&x)[2], float sg, float su) {
+        float d[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const uint32_t wg = j < 2 ? cg.x : cg.y, wu = j < 2 ? cu.x : cu.y;
             const int k = 2 * (j & 1);
             const uint32_t a0 = few_pair(wg, k, tl), a1 = few_pair(wu, k, tl);
             const uint32_t a2 = few_pair(wg, k + 1, tl), a3 = few_pair(wu, k + 1, tl);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const uint4 v = x[n][j >> 1];
-                const uint32_t b0 = j & 1 ? v.z : v.x, b1 = j & 1 ? v.w : v.y;
-                if (j == 0)
-                    mma_16816_z(d[n], a0, a1, a2, a3, b0, b1);
-                else
-                    mma_16816(d[n], a0, a1, a2, a3, b0, b1);
-            }
+            const uint4 v = x[j >> 1];
+            if (j == 0)
+                mma_16816_z(d, a0, a1, a2, a3, v.x, v.y);
+            else
+                mma_16816(d, a0, a1, a2, a3, j & 1 ? v.z : v.x, j & 1 ? v.w : v.y);
         }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            acc[n][0] = __fmaf_rn(sg, d[n][0], acc[n][0]);
-            acc[n][1] = __fmaf_rn(sg, d[n][1], acc[n][1]);
-            acc[n][2] = __fmaf_rn(su, d[n][2], acc[n][2]);
-            acc[n][3] = __fmaf_rn(su, d[n][3], acc[n][3]);
-        }
+        acc[0] = __fmaf_rn(sg, d[0], acc[0]);
+        acc[1] = __fmaf_rn(sg, d[1], acc[1]);
+        acc[2] = __fmaf_rn(su, d[2], acc[2]);
+        acc[3] = __fmaf_rn(su, d[3], acc[3]);
     };
 
     while (true) {
         Pos u = start();
-        int xq = -1;
-        uint4 x[4][NT][2];
         auto step = [&](const Raw& v, int st) {
             if (u.q != xq) {
                 xq = u.q;
@@ -259,16 +280,9 @@ __global__ void __launch_bounds__(GatedFewShape<NT>::THREADS, 1) k_gated_few(con
                 for (int i = 0; i < 4; ++i) load_x(x[i], 4 * xq + i);
             }
             const float sc0 = block_const(v.s[0], v.q[0]), sc1 = block_const(v.s[1], v.q[1]);
-            float acc[NT][4];
-            float4* slot = part + ((u.e * (W + 1) + warp) * NT) * 32 + lane;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float4 o = u.q >= W ? slot[n * 32] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                acc[n][0] = o.x;
-                acc[n][1] = o.y;
-                acc[n][2] = o.z;
-                acc[n][3] = o.w;
-            }
+            float4* slot = part + (u.e * (W + 1) + warp) * 32 + lane;
+            const float4 o = u.q >= W ? *slot : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float acc[4] = {o.x, o.y, o.z, o.w};
             const uint32_t row = ring + (uint32_t)(st * S::STAGE) + (uint32_t)(gid * 128 + tig * 4) + ((uint32_t)gid << 4);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -277,8 +291,7 @@ __global__ void __launch_bounds__(GatedFewShape<NT>::THREADS, 1) k_gated_few(con
                       make_uint2(ld_shared_u32(c0 + S::STAGE / 2), ld_shared_u32(c1 + S::STAGE / 2)), x[i],
                       __shfl_sync(0xffffffffu, sc0, (lane & 28) | i), __shfl_sync(0xffffffffu, sc1, (lane & 28) | i));
             }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) slot[n * 32] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+            *slot = make_float4(acc[0], acc[1], acc[2], acc[3]);
             advance(u);
         };
         // (the stages take turns: the loop is unrolled by their number)
@@ -305,11 +318,7 @@ __global__ void __launch_bounds__(GatedFewShape<NT>::THREADS, 1) k_gated_few(con
         // the block columns after the last whole unit
         if (rem)
             for (int e = warp; e < n_items; e += W) {
-                float acc[NT][4];
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[n][j] = 0.0f;
+                float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 const int64_t row = (int64_t)(item0 + e) * 8 + gid;
 #pragma unroll 1
                 for (int kb = 4 * Q; kb < p.kbs; ++kb) {
@@ -319,15 +328,13 @@ __global__ void __launch_bounds__(GatedFewShape<NT>::THREADS, 1) k_gated_few(con
                     const uint32_t b = (uint32_t)(((item0 - i_begin + e) * 8 + gid) * p.kbs + kb);
                     load_const(bg, b, s0, v0);
                     load_const(bu, b, s1, v1);
-                    uint4 xr[NT][2];
+                    uint4 xr[2];
                     load_x(xr, kb);
                     auto word = [&](int64_t o) { return *reinterpret_cast<const uint32_t*>(c + o); };
                     block(acc, make_uint2(word(0), word(16)), make_uint2(word(up_c), word(up_c + 16)), xr,
                           block_const(s0, v0), block_const(s1, v1));
                 }
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    part[((e * (W + 1) + W) * NT + n) * 32 + lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+                part[(e * (W + 1) + W) * 32 + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
             }
         if (p.r > 0) pdl_wait();  // sU
         __syncthreads();
@@ -337,49 +344,46 @@ __global__ void __launch_bounds__(GatedFewShape<NT>::THREADS, 1) k_gated_few(con
             const int w0 = Q < W ? (e % NG) * Q : 0, cnt = min(Q, W);
             const int f = (item0 + e) * 8 + gid;
             const int64_t fg = (int64_t)f * p.r, fu = ((int64_t)p.F + f) * p.r;
+            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            auto add = [&](int w) {
+                const float4 o = part[(e * (W + 1) + w) * 32 + lane];
+                v[0] = __fadd_rn(v[0], o.x);
+                v[1] = __fadd_rn(v[1], o.y);
+                v[2] = __fadd_rn(v[2], o.z);
+                v[3] = __fadd_rn(v[3], o.w);
+            };
+            for (int j = 0; j < cnt; ++j) add(w0 + j);
+            if (rem) add(W);
+            const int64_t tu = (int64_t)min(gid, p.M - 1) * 2 * p.r;
+            for (int j0 = 0; j0 < p.r; j0 += 32) {
+                const int j = j0 + 8 * tig;
+                const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+                const bool on = j < p.r;
+                const uint4 b0 = on ? *reinterpret_cast<const uint4*>(p.B + fg + j) : z;
+                const uint4 b1 = on ? *reinterpret_cast<const uint4*>(p.B + fu + j) : z;
+                const uint4 u0 = on ? *reinterpret_cast<const uint4*>(p.sU + tu + j) : z;
+                const uint4 u1 = on ? *reinterpret_cast<const uint4*>(p.sU + tu + p.r + j) : z;
+                mma_16816(v, b0.x, 0u, b0.y, 0u, u0.x, u0.y);
+                mma_16816(v, b0.z, 0u, b0.w, 0u, u0.z, u0.w);
+                mma_16816(v, 0u, b1.x, 0u, b1.y, u1.x, u1.y);
+                mma_16816(v, 0u, b1.z, 0u, b1.w, u1.z, u1.w);
+            }
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                auto add = [&](int w) {
-                    const float4 o = part[((e * (W + 1) + w) * NT + n) * 32 + lane];
-                    v[0] = __fadd_rn(v[0], o.x);
-                    v[1] = __fadd_rn(v[1], o.y);
-                    v[2] = __fadd_rn(v[2], o.z);
-                    v[3] = __fadd_rn(v[3], o.w);
-                };
-                for (int j = 0; j < cnt; ++j) add(w0 + j);
-                if (rem) add(W);
-                const int64_t tu = (int64_t)min(8 * n + gid, p.M - 1) * 2 * p.r;
-                for (int j0 = 0; j0 < p.r; j0 += 32) {
-                    const int j = j0 + 8 * tig;
-                    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-                    const bool on = j < p.r;
-                    const uint4 bg = on ? *reinterpret_cast<const uint4*>(p.B + fg + j) : z;
-                    const uint4 bu = on ? *reinterpret_cast<const uint4*>(p.B + fu + j) : z;
-                    const uint4 ug = on ? *reinterpret_cast<const uint4*>(p.sU + tu + j) : z;
-                    const uint4 uu = on ? *reinterpret_cast<const uint4*>(p.sU + tu + p.r + j) : z;
-                    mma_16816(v, bg.x, 0u, bg.y, 0u, ug.x, ug.y);
-                    mma_16816(v, bg.z, 0u, bg.w, 0u, ug.z, ug.w);
-                    mma_16816(v, 0u, bu.x, 0u, bu.y, uu.x, uu.y);
-                    mma_16816(v, 0u, bu.z, 0u, bu.w, uu.z, uu.w);
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int m = 8 * n + 2 * tig + h;
-                    if (m >= p.M || abort_flag || !QLORA_CHECK(f < p.F)) continue;
-                    const float g = v[h], u1 = v[2 + h];
-                    const float y = (p.act == ACT_SILU ? act_value(ACT_SILU, g) : act_value(ACT_GELU_TANH, g)) * u1;
-                    p.H[(int64_t)m * p.F + f] = (uint16_t)(pack_bf16x2(y, 0.0f) & 0xFFFFu);
-                    if (p.GU) {
-                        p.GU[(int64_t)m * 2 * p.F + f] = (uint16_t)(pack_bf16x2(g, 0.0f) & 0xFFFFu);
-                        p.GU[(int64_t)m * 2 * p.F + p.F + f] = (uint16_t)(pack_bf16x2(u1, 0.0f) & 0xFFFFu);
-                    }
+            for (int h = 0; h < 2; ++h) {
+                const int m = 2 * tig + h;
+                if (m >= p.M || abort_flag || !QLORA_CHECK(f < p.F)) continue;
+                const float g = v[h], u1 = v[2 + h];
+                const float y = (p.act == ACT_SILU ? act_value(ACT_SILU, g) : act_value(ACT_GELU_TANH, g)) * u1;
+                p.H[(int64_t)m * p.F + f] = (uint16_t)(pack_bf16x2(y, 0.0f) & 0xFFFFu);
+                if (p.GU) {
+                    p.GU[(int64_t)m * 2 * p.F + f] = (uint16_t)(pack_bf16x2(g, 0.0f) & 0xFFFFu);
+                    p.GU[(int64_t)m * 2 * p.F + p.F + f] = (uint16_t)(pack_bf16x2(u1, 0.0f) & 0xFFFFu);
                 }
             }
         }
-        item0 += S::CHUNK;
+        item0 += chunk;
         if (item0 >= i_end) break;
-        n_items = min(S::CHUNK, i_end - item0);
+        n_items = min(chunk, i_end - item0);
         next = start();
         if (!dead) {
 #pragma unroll

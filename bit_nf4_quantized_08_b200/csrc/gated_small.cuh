@@ -1,5 +1,5 @@
-// gated_small.cuh -- the gated feed-forward's forward for few tokens (M <= 128:
-// decoding and small batches), where the frozen weight is streamed once and
+// gated_small.cuh -- the gated feed-forward's forward for 9 to 128 tokens
+// (decoding in batches), where the frozen weight is streamed once and
 // the NF4 expansion sets the pace.
 //
 //   H = act(g) u,   [g | u] = X W'^T + sU B^T  (adapters of the two halves)
@@ -32,7 +32,7 @@
 // the hand-overs between loads, expansion and products, not by HBM: codes and
 // constants are 46 MB on LLaMA-7B (7 us) and 186 MB on LLaMA-65B (28 us).
 // Measured with cold caches, kernel alone: LLaMA-65B 133 us at 48 tokens (1.4
-// TB/s), LLaMA-7B 44 us at one (1.1 TB/s).  With two groups instead of three
+// TB/s), LLaMA-7B 44 us at 16 or fewer (1.1 TB/s).  With two groups instead of three
 // 65B took 151 us; two block columns a slot, 128-byte code lines, or a table of
 // code pairs in shared memory instead of the byte permutes were no faster.
 #pragma once

@@ -1000,8 +1000,12 @@ inline qlora_status linear_bwd_impl(const void* dY, const void* X, const LinearA
 // with cold caches: LLaMA-7B 128 / 129 tokens 113 / 111 us, LLaMA-65B 186 /
 // 285 us; at 16 tokens 7B 50 us, 65B 133 us.
 constexpr int kGatedSmall = 128;
-// Most tokens of k_gated_few.
-constexpr int kGatedFew = 16;
+// Most tokens of k_gated_few (its MMA's token side; with two token tiles a warp
+// LLaMA-65B took 147 us at 16 tokens against 133 us for k_gated_small,
+// LLaMA-7B 51 us against 50 us).  At 8 tokens it takes 84 us on LLaMA-65B
+// against 131 us, at one on LLaMA-7B 31 us against 49 us (whole calls, cold
+// caches).
+constexpr int kGatedFew = 8;
 
 struct BlockWs {
     void* linear;
@@ -1070,17 +1074,6 @@ inline qlora_status launch_sU(const void* X, const LinearArgs& a, const void* A,
     return skinny(&d, 1, a.rt(), s, 1);
 }
 
-template <int NT>
-inline cudaError_t launch_gated_few_kernel(const GatedFewParams& p, int grid, cudaStream_t s) {
-    using S = GatedFewShape<NT>;
-    auto kern = k_gated_few<NT>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
-    if (e != cudaSuccess) return e;
-    ProfileScope ps(QLORA_KERNEL_SMALLM_GEMM, s);
-    note_launch();
-    return launch_pdl(kern, dim3((unsigned)grid, 1, 1), dim3(S::THREADS, 1, 1), S::SMEM, s, 0, p);
-}
-
 // H = act(g) u for M <= kGatedFew: a range of hidden columns per SM.
 inline qlora_status gated_fwd_few(const void* X, const LinearArgs& a, const void* A, const void* B, int act, void* H,
                                   void* GU, const BlockWs& b, cudaStream_t s) {
@@ -1114,8 +1107,18 @@ inline qlora_status gated_fwd_few(const void* X, const LinearArgs& a, const void
     p.H = static_cast<uint16_t*>(H);
     p.GU = static_cast<uint16_t*>(GU);
     const int grid = (int)std::min<int64_t>(std::min(sm_count(), kSms), a.seg_rows / 8);
-    const cudaError_t e = a.M <= 8 ? launch_gated_few_kernel<1>(p, grid, s) : launch_gated_few_kernel<2>(p, grid, s);
-    return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+    // k_small_u holds rt / 8 SMs for about 3 us after this kernel could start,
+    // the time of some 28 of an SM's units
+    p.late = a.r > 0 && !a.drop && a.rt() / 8 < grid ? a.rt() / 8 : 0;
+    p.less = (28 + p.kbs / 8) / std::max(p.kbs / 4, 1);
+    using S = GatedFewShape;
+    if (cudaFuncSetAttribute(k_gated_few, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM) != cudaSuccess)
+        return QLORA_ERR_CUDA;
+    ProfileScope ps(QLORA_KERNEL_SMALLM_GEMM, s);
+    note_launch();
+    return launch_pdl(k_gated_few, dim3((unsigned)grid, 1, 1), dim3(S::THREADS, 1, 1), S::SMEM, s, 0, p) == cudaSuccess
+               ? QLORA_OK
+               : QLORA_ERR_CUDA;
 }
 
 // H = act(g) u for M <= kGatedSmall on a persistent stream-K grid (one CTA per
