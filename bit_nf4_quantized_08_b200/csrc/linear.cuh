@@ -991,8 +991,8 @@ inline qlora_status linear_bwd_impl(const void* dY, const void* X, const LinearA
 }
 
 // ---------------------------------------------------------------------------
-// The gated feed-forward.  Workspace: forward, sU and, for few tokens, the
-// partial tiles and their arrival counters, else the expanded block constants;
+// The gated feed-forward.  Workspace: forward, sU and, for 9 to 128 tokens, the
+// partial tiles and their arrival counters, for more the expanded block constants;
 // backward, the linear's, the gradient of the pre-activations [M, 2F] and the
 // split partial sums of sG.
 // ---------------------------------------------------------------------------
@@ -1026,6 +1026,8 @@ inline BlockWs carve_block_ws(void* ws, int64_t M, int64_t N, int64_t K, int rt,
     WsCarve c{static_cast<char*>(ws), 0};
     if (!bwd && M <= kGatedSmall) {
         b.sU = rt > 0 ? static_cast<uint16_t*>(c.take((size_t)M * rt * 2)) : nullptr;
+        b.bytes = c.used;
+        if (M <= kGatedFew) return b;
         b.part_floats = (size_t)kSms * 2 * M * 256;
         b.part = static_cast<float*>(c.take(b.part_floats * 4));
         b.counters = static_cast<unsigned long long*>(c.take((size_t)(N / 256) * 8));

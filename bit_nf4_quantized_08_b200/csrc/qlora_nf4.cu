@@ -520,7 +520,7 @@ qlora_status qlora_gated_linear_fwd(const void* X, int64_t M, const qlora_nf4_we
     if (!X || !aligned(X, 16) || !H || !aligned(H, 16) || !aligned(GU, 16) || !adapter_ok(A, B, r))
         return QLORA_ERR_INVALID_ARG;
     const size_t need = carve_block_ws(nullptr, M, w->rows, w->cols, 2 * r, 0).bytes;
-    if (!ws || !aligned(ws, 16) || ws_bytes < need) return QLORA_ERR_INVALID_ARG;
+    if (need > 0 && (!ws || !aligned(ws, 16) || ws_bytes < need)) return QLORA_ERR_INVALID_ARG;
     LinearArgs a{M, w->rows, w->cols, r, dropped_scale(scale, d), w, 2, w->rows / 2,
                  d.thr && r > 0 ? &d : nullptr, 0, 0, nullptr};
     return gated_fwd_impl(X, a, A, B, act, H, GU, ws, reinterpret_cast<cudaStream_t>(stream));

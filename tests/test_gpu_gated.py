@@ -423,3 +423,18 @@ def test_gated_token_of_nan_stays_in_its_row(Q, cuda, M):
     assert Q.qlora_get_last_error() == 0
     for a, b in zip(*outs):
         assert _same_bits(a[rows], b[rows]) and torch.isnan(b[bad]).all()
+
+
+@pytest.mark.parametrize("F,K,r", [
+    (256, 256, 8),     # one unit column, every warp on it
+    (512, 704, 72),    # two unit columns and three blocks after them, adapters ending inside a k-step
+    (768, 2240, 128),  # eight unit columns, two warps each
+    (256, 4416, 24),   # seventeen: a warp has two of them
+    (9728, 576, 16),   # more hidden columns an SM than fit one reduction
+    (512, 128, 0),     # no whole unit, no adapter
+])
+@pytest.mark.parametrize("M", [1, 5, 8])
+def test_gated_few_tokens(Q, O, cuda, M, F, K, r):
+    q, inp, Wd = _setup(Q, M, F, K, r, seed=200 + M)
+    drop = Q.Dropout(0.2, 5, M) if r and M == 5 else None
+    _check(Q, O, q, inp, Wd, 2.0, "gelu_tanh" if M == 8 else "silu", drop, f"few M={M} F={F} K={K} r={r}")
