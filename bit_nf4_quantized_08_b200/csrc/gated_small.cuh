@@ -38,6 +38,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "dropout.cuh"
 #include "gated.cuh"
 #include "gemm.cuh"
 #include "nf4.cuh"
@@ -529,8 +530,9 @@ __global__ void __launch_bounds__(GatedSmallShape<TOK>::THREADS, 1)
 }
 
 // ---------------------------------------------------------------------------
-// sU = bf16(scale X A^T) for up to 16 tokens, ahead of k_gated_small.  A CTA
-// takes eight adapter rows, its 32 warps the 64-element block columns in turn;
+// sU = bf16(scale X A^T) for up to 16 tokens, ahead of the gated kernels and,
+// under dropout, of the linear's (DROP: X masked in registers; every CTA forms
+// the whole mask, 2.6 us of generator for 16 tokens of 4096).  A CTA takes eight adapter rows, its 32 warps the 64-element block columns in turn;
 // within a block thread t of a fragment's group of four holds elements
 // 16 t .. 16 t + 15 of its rows for both operands, so that every load is 16
 // contiguous bytes (a sum over k does not depend on its order).  The warps'
@@ -540,8 +542,9 @@ __global__ void __launch_bounds__(GatedSmallShape<TOK>::THREADS, 1)
 // holds eight SMs' shared memory for that long.  (For more tokens its tiles
 // are better: 27 us here against 14 us for 48 tokens, LLaMA-65B.)
 // ---------------------------------------------------------------------------
+template <bool DROP>
 __global__ void __launch_bounds__(1024) k_small_u(const uint16_t* X, const uint16_t* A, uint16_t* U, int M, int K, int rt,
-                                                  float scale) {
+                                                  float scale, const __grid_constant__ DropParams d) {
     __shared__ float part[32][16][8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
     pdl_wait();
@@ -552,11 +555,29 @@ __global__ void __launch_bounds__(1024) k_small_u(const uint16_t* X, const uint1
     const uint4* x1 = reinterpret_cast<const uint4*>(X + (int64_t)(gid + 8) * K + tig * 16);
     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll 2
+    const DropCtx ctx = DROP ? drop_ctx(d, drop_offset(d), 0u) : DropCtx{};
+    // the 16 elements of row m from column k (16 rows of less than 2^31: the
+    // block number fits in 32 bits)
+    auto mask = [&](uint4 (&x)[2], int m, int k) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t b[4];
+            drop_mask8(d, ctx, (uint32_t)(((int64_t)m * K + k) >> 3) + h, b);
+            x[h].x &= b[0];
+            x[h].y &= b[1];
+            x[h].z &= b[2];
+            x[h].w &= b[3];
+        }
+    };
+#pragma unroll(DROP ? 1 : 2)
     for (int kb = warp; kb < K / 64; kb += 32) {
         const uint4 b[2] = {av[kb * 8], av[kb * 8 + 1]};
-        const uint4 lo[2] = {gid < M ? x0[kb * 8] : zero, gid < M ? x0[kb * 8 + 1] : zero};
-        const uint4 hi[2] = {gid + 8 < M ? x1[kb * 8] : zero, gid + 8 < M ? x1[kb * 8 + 1] : zero};
+        uint4 lo[2] = {gid < M ? x0[kb * 8] : zero, gid < M ? x0[kb * 8 + 1] : zero};
+        uint4 hi[2] = {gid + 8 < M ? x1[kb * 8] : zero, gid + 8 < M ? x1[kb * 8 + 1] : zero};
+        if (DROP) {
+            mask(lo, gid, kb * 64 + tig * 16);
+            if (M > 8) mask(hi, gid + 8, kb * 64 + tig * 16);
+        }
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             mma_16816(acc, lo[c].x, hi[c].x, lo[c].y, hi[c].y, b[c].x, b[c].y);
