@@ -102,8 +102,9 @@ __global__ void __launch_bounds__(256) k_gated_grad(const uint16_t* dH, const ui
 // A CTA owns 128 tokens x a range of 64-column steps.  Per step sixteen warps
 // form dG and dU [128 x 64] from dH, g and u, which they load into registers
 // two steps ahead (96 KB in flight an SM: 2.2 us a step; with all three through
-// a TMA ring in shared memory, three steps deep, it was 3.2 us), and write them to an operand stage; one thread stores the two tiles
-// with TMA, one loads the two adapters' B rows and one issues the tcgen05
+// a TMA ring in shared memory, three steps deep, it was 3.2 us), and write them
+// to an operand stage; one thread stores the two tiles with TMA, one loads the
+// two adapters' B rows and one issues the tcgen05
 // products onto two accumulators [128 x r].  The column range is split over S
 // CTAs (about one CTA an SM in all), whose fp32 partial sums k_gated_sG adds in
 // split order (deterministic) and rounds once (added by each token tile's last

@@ -532,11 +532,12 @@ __global__ void __launch_bounds__(GatedSmallShape<TOK>::THREADS, 1)
 // ---------------------------------------------------------------------------
 // sU = bf16(scale X A^T) for up to 16 tokens, ahead of the gated kernels and,
 // under dropout, of the linear's (DROP: X masked in registers; every CTA forms
-// the whole mask, 2.6 us of generator for 16 tokens of 4096).  A CTA takes eight adapter rows, its 32 warps the 64-element block columns in turn;
-// within a block thread t of a fragment's group of four holds elements
-// 16 t .. 16 t + 15 of its rows for both operands, so that every load is 16
-// contiguous bytes (a sum over k does not depend on its order).  The warps'
-// sums are added in warp order.
+// the whole mask, some 2.6 us of generator for 16 tokens of 4096).  A CTA takes
+// eight adapter rows, its 32 warps the 64-element block columns in turn; within
+// a block thread t of a fragment's group of four holds elements 16 t .. 16 t +
+// 15 of its rows for both operands, so that every load is 16 contiguous bytes
+// (a sum over k does not depend on its order).  The warps' sums are added in
+// warp order.
 // Bound by latency: 1 to 2 MB of A through 2r / 8 CTAs, 4.6 us on LLaMA-7B
 // against 11 us for the TMA-fed cluster kernel of larger batches, which also
 // holds eight SMs' shared memory for that long.  (For more tokens its tiles

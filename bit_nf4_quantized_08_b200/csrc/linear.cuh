@@ -871,6 +871,8 @@ inline bool side_fork_ok() { return large_m_schedule() == SCHED_PAIR; }
 //         its LoRA k-step) -> wait for the side stream
 //   side: wait for sG -> sU -> dA, dB (one CTA per tile each), on the SMs the
 //         GEMM leaves free
+// Under adapter dropout sG (and perhaps sU) comes first, with the expansion
+// beside it; in the gated backward its first pass has formed sG.
 inline qlora_status linear_bwd_forked(const void* dY, const void* X, const LinearArgs& a, const void* A,
                                       const void* B, void* dX, void* dA, void* dB, const LinearWs& L,
                                       const CUtensorMap& tdY, const SideStream& side, cudaStream_t s) {
@@ -919,8 +921,8 @@ inline qlora_status linear_bwd_forked(const void* dY, const void* X, const Linea
     // dropout: sG, the counters and perhaps sU do)
     if (st == QLORA_OK)
         st = sU_first ? skinny(d3 + 1, 2, a.rt(), side.st, 1, SKP_STREAM, sm_count(), L.sk_flags + kMaxStreamK)
-                      : skinny(d3, 3, a.rt(), side.st, a.have_sG || a.drop, SKP_STREAM, sm_count(), L.sk_flags + kMaxStreamK, 2,
-                               1 << 1);
+                      : skinny(d3, 3, a.rt(), side.st, a.have_sG || a.drop, SKP_STREAM, sm_count(),
+                               L.sk_flags + kMaxStreamK, 2, 1 << 1);
     if (cudaEventRecord(side.join, side.st) != cudaSuccess || cudaStreamWaitEvent(s, side.join, 0) != cudaSuccess)
         st = QLORA_ERR_CUDA;
     return st;
@@ -1016,7 +1018,7 @@ inline qlora_status linear_bwd_impl(const void* dY, const void* X, const LinearA
 // ---------------------------------------------------------------------------
 // Most tokens of k_gated_small (its MMA's token side).  Around it, whole calls
 // with cold caches: LLaMA-7B 128 / 129 tokens 113 / 111 us, LLaMA-65B 186 /
-// 285 us; at 16 tokens 7B 50 us, 65B 133 us.
+// 285 us.
 constexpr int kGatedSmall = 128;
 // Most tokens of k_gated_few (its MMA's token side; with two token tiles a warp
 // LLaMA-65B took 147 us at 16 tokens against 133 us for k_gated_small,
