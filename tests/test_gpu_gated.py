@@ -438,3 +438,44 @@ def test_gated_few_tokens(Q, O, cuda, M, F, K, r):
     q, inp, Wd = _setup(Q, M, F, K, r, seed=200 + M)
     drop = Q.Dropout(0.2, 5, M) if r and M == 5 else None
     _check(Q, O, q, inp, Wd, 2.0, "gelu_tanh" if M == 8 else "silu", drop, f"few M={M} F={F} K={K} r={r}")
+
+
+@pytest.mark.parametrize("M", [1, 8, 12])
+def test_gated_few_tokens_captured(Q, cuda, M):
+    """A captured decoding call replayed on new inputs, after calls of other sizes in the same workspace."""
+    q, inp, _ = _setup(Q, M, 1024, 512, 16, seed=41)
+    t = _dev(inp)
+    ws = torch.full((Q.qlora_gated_linear_workspace(128, q, 16, False),), 0xFF, dtype=torch.uint8, device=cuda)
+    X = t["X"].clone()
+    H = torch.empty(M, 1024, dtype=torch.bfloat16, device=cuda)
+
+    def call(x, out):
+        return Q.qlora_gated_linear_fwd(x, q, t["A"], t["B"], 2.0, H=out, ws=ws)[0]
+
+    call(X, H)
+    g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s), torch.cuda.graph(g, stream=s):
+        call(X, H)
+    for i in range(3):
+        X.copy_(t["X"] * (i + 1))
+        Q.qlora_gated_linear_fwd(t["X"].repeat(40 // M + 1, 1), q, t["A"], t["B"], 2.0, ws=ws)
+        g.replay()
+        assert _same_bits(H, call(X, torch.empty_like(H))), i
+    torch.cuda.synchronize()
+    assert Q.qlora_get_last_error() == 0
+
+
+def test_gated_without_workspace(Q, cuda):
+    """Up to 8 tokens without an adapter need no workspace: the query gives 0 and the call takes NULL."""
+    import ctypes
+
+    from bit_nf4_quantized_08_b200 import _lib
+    q, inp, _ = _setup(Q, 8, 256, 320, 0, seed=42)
+    X = inp["X"].cuda()
+    assert Q.qlora_gated_linear_workspace(8, q, 0, False) == 0
+    H = torch.empty(8, 256, dtype=torch.bfloat16, device=cuda)
+    st = _lib.lib().qlora_gated_linear_fwd(X.data_ptr(), 8, ctypes.byref(q.c_struct()), None, None, 0, 1.0, 0, None,
+                                           H.data_ptr(), None, None, 0, torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    assert _same_bits(H, Q.qlora_gated_linear_fwd(X, q, None, None, 1.0)[0])
