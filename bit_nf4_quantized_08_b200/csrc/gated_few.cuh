@@ -7,8 +7,11 @@
 // As in the plain linear for few tokens, the block constant is factored out of
 // each 64-element block, so that the inner sums are warp MMAs (m16n8k16) whose
 // weight operand comes from a table of code-byte pairs, one shared-memory load
-// a register (smallm_mma.cuh has the table, its prescale and the permutation of
-// k).  Here the weight is the 16-row operand: 8 gate rows and the 8 up rows of
+// a register (smallm_mma.cuh has the table and its prescale).  The table's 16
+// values are rounded to bf16, the operand type of the MMA: at most 1.6e-3 of a
+// value, which puts H at 3.4e-3 of its definition instead of 1.8e-3; a second
+// table for the remainders would double the lookups that bound the kernel.
+// Block constants, sums, activation and product are fp32.  Here the weight is the 16-row operand: 8 gate rows and the 8 up rows of
 // the same hidden columns, so that a thread ends with g and u of one column
 // and forms H, and the tokens are the 8-column operand.
 //
