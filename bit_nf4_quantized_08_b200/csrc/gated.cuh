@@ -33,12 +33,20 @@ __device__ __forceinline__ float sigmoid_f(float x) {
     return r;
 }
 
+// g clamped to [-32, 32]; a NaN stays NaN (fminf and fmaxf would drop it).
+__device__ __forceinline__ float clamp32(float g) {
+    float x;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(g), "f"(-32.0f));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(x), "f"(32.0f));
+    return x;
+}
+
 // act(g) and act'(g).
 __device__ __forceinline__ float act_value(int act, float g) {
     if (act == ACT_SILU) return g * sigmoid_f(g);
     // (1 + tanh y) / 2 = sigma(2 y); at |g| = 32 it is 0 or 1 in fp32, and the
     // clamp keeps the cubic finite for every g
-    const float x = fminf(fmaxf(g, -32.0f), 32.0f);
+    const float x = clamp32(g);
     return g * sigmoid_f(2.0f * 0.7978845608028654f * x * (1.0f + 0.044715f * x * x));
 }
 __device__ __forceinline__ void act_value_grad(int act, float g, float* v, float* dv) {
@@ -48,7 +56,7 @@ __device__ __forceinline__ void act_value_grad(int act, float g, float* v, float
         *dv = s * (1.0f + g * (1.0f - s));
         return;
     }
-    const float x = fminf(fmaxf(g, -32.0f), 32.0f), g2 = x * x;
+    const float x = clamp32(g), g2 = x * x;
     const float s = sigmoid_f(2.0f * 0.7978845608028654f * x * (1.0f + 0.044715f * g2));
     *v = g * s;
     // d/dg g sigma(2 y) = sigma + g 2 y' sigma (1 - sigma), y' = c (1 + 3 * 0.044715 g^2)
