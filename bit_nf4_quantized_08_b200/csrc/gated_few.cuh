@@ -4,16 +4,19 @@
 //
 //   H = act(g) u,   [g | u] = X W'^T + sU B^T
 //
-// As in the plain linear for few tokens, the block constant is factored out of
-// each 64-element block, so that the inner sums are warp MMAs (m16n8k16) whose
-// weight operand comes from a table of code-byte pairs, one shared-memory load
-// a register (smallm_mma.cuh has the table and its prescale).  The table's 16
-// values are rounded to bf16, the operand type of the MMA: at most 1.6e-3 of a
-// value, which puts H at 3.4e-3 of its definition instead of 1.8e-3; a second
-// table for the remainders would double the lookups that bound the kernel.
-// Block constants, sums, activation and product are fp32.  Here the weight is the 16-row operand: 8 gate rows and the 8 up rows of
-// the same hidden columns, so that a thread ends with g and u of one column
-// and forms H, and the tokens are the 8-column operand.
+// The inner sums are warp MMAs (m16n8k16) whose weight operand is formed in
+// registers: a table of code-byte pairs in shared memory gives the two fp32
+// code values of a byte with one load, which are multiplied by the block
+// constant and rounded to bf16.  That is qlora_nf4_dequantize's weight bit for
+// bit, so that the block is the same function whatever the token count and its
+// backward differentiates what its forward computed.  (With the code book
+// itself rounded to bf16 and the constant applied to each block's sum, as in
+// the plain linear for few tokens, H was 3.4e-3 off its definition instead of
+// 1.7e-3, in 33 us instead of 39 us on LLaMA-7B and 84 instead of 102 us on
+// LLaMA-65B.)  Sums, activation and product are fp32.  The weight is the
+// 16-row operand: 8 gate rows and the 8 up rows of the same hidden columns, so
+// that a thread ends with g and u of one column and forms H, and the tokens
+// are the 8-column operand.
 //
 // A unit is (8 hidden columns, 256 elements of k): 16 lines of 128 bytes of
 // codes.  A CTA owns a range of hidden columns and each of its 16 warps some
@@ -29,14 +32,16 @@
 // and 32 + 8 t .. + 7): a load of one word a lane then covers a 16-byte chunk of
 // eight rows, which the 128-byte swizzle spreads over all banks.
 //
-// Bound by shared memory: about 34 wavefronts for a 64-element block of 16 rows,
-// 16 of them table lookups, keep that pipe busy for 62 % of the time, and the
-// latencies of 16 warps a SM take most of the rest; HBM (28 us on LLaMA-65B, 7
-// us on LLaMA-7B) does not.  One token, cold caches, kernel alone: LLaMA-65B 75
-// us (2.5 TB/s), LLaMA-7B 25 us (1.8 TB/s; about 9 us of it are start, table,
-// adapters and end).  On LLaMA-65B it was 105 us with codes and constants
-// loaded straight into registers, X read per block and a two-instruction table
-// address, and 92 us with X kept in registers.
+// Bound by shared memory: 51 wavefronts for a 64-element block of 16 rows, 32 of
+// them table lookups (two for a warp's 64-bit loads), keep that pipe busy for
+// 69 % of the time, and the latencies of 16 warps a SM take most of the rest;
+// HBM (28 us on LLaMA-65B, 7 us on LLaMA-7B) does not.  One token, kernel
+// alone: LLaMA-65B 97 us (1.9 TB/s), LLaMA-7B 32 us (1.5 TB/s; about 9 us of it
+// are start, table, adapters and end).  k_gated_small takes 116 and 46 us
+// there.  (Steps towards it, measured with the rounded code book: on LLaMA-65B
+// 105 us with codes and constants loaded straight into registers, X read per
+// block and a two-instruction table address, 92 us with X kept in registers, 78
+// us with codes through TMA rings.)
 #pragma once
 
 #include "common.cuh"
@@ -59,7 +64,6 @@ struct GatedFewParams {
     int dq;
     int F, M, K, kbs;      // kbs = K / 64
     int r, act;
-    float inv_scale;       // 1 / the table's prescale
     QFormat fmt;
     uint16_t* H;           // [M][F]
     uint16_t* GU;          // [M][2F] or nullptr
@@ -74,7 +78,7 @@ struct GatedFewShape {
     static constexpr int STAGES = 3;                 // of a warp's ring
     static constexpr int STAGE = 2048;               // 8 gate and 8 up rows of 128 bytes
     static constexpr int CHUNK = 7;                  // most items (8 hidden columns) between two reductions
-    static constexpr int LUT_BYTES = 256 * 256;      // entry e of lane l at 256 e + 4 l
+    static constexpr int LUT_BYTES = 256 * 256;      // entry e of lane l at 256 e + 8 l
     static constexpr int RING_BYTES = WARPS * STAGES * STAGE;
     static constexpr int PART_BYTES = CHUNK * (WARPS + 1) * 32 * 16;  // [item of the chunk][warp or remainder][lane]
     // partial sums up to address 65536, the table, the rings (a window's first 1 KB is the system's)
@@ -87,13 +91,19 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
     return v;
 }
-// The pair of bf16 table values of byte k of w.  The table starts at a multiple
-// of 64 KB, which tl (this lane's column of the first entry) holds in its upper
-// half: one byte permute forms the address.
-__device__ __forceinline__ uint32_t few_pair(uint32_t w, int k, uint32_t tl) {
-    uint32_t v;
-    asm("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(prmt(w, tl, 0x7604u | (uint32_t)(k << 4))));
-    return v;
+// The two weights of code byte k of w, bf16(code * a) as qlora_nf4_dequantize
+// rounds them; a2 holds the block constant a twice.  The table starts at a
+// multiple of 64 KB, which tl (this lane's column of the first entry) holds in
+// its upper half: one byte permute forms the address.
+__device__ __forceinline__ uint32_t few_pair(uint32_t w, int k, uint32_t tl, uint64_t a2) {
+    uint64_t v;
+    asm("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(prmt(w, tl, 0x7604u | (uint32_t)(k << 4))));
+    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(a2));
+    return pack_bf16x2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+}
+
+__device__ __forceinline__ uint64_t twice(float a) {
+    return (uint64_t)__float_as_uint(a) << 32 | __float_as_uint(a);
 }
 
 __global__ void __launch_bounds__(GatedFewShape::THREADS, 1) k_gated_few(const __grid_constant__ GatedFewParams p) {
@@ -107,7 +117,7 @@ __global__ void __launch_bounds__(GatedFewShape::THREADS, 1) k_gated_few(const _
     __shared__ __align__(8) uint64_t full_bar[W * S::STAGES];
     __shared__ volatile int abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
-    const uint32_t tl = lut + (uint32_t)lane * 4u;
+    const uint32_t tl = lut + (uint32_t)lane * 8u;
     const int items = p.F / 8;
     // The last `late` CTAs find their SM when the kernel that forms sU has left
     // it, and take `less` items fewer than the others.
@@ -238,40 +248,29 @@ __global__ void __launch_bounds__(GatedFewShape::THREADS, 1) k_gated_few(const _
         }
     }
     // the table and the 8-bit code book, while the first loads are on their way
-    {
-        const float L = small_m_table_scale(p.fmt.code_type);
-        for (int e = warp; e < 256; e += W)
-            *reinterpret_cast<uint32_t*>(smem_raw + (tl - dyn) + 256 * e) =
-                pack_bf16x2(__fmul_rn(code_value(p.fmt.code_type, e >> 4), L),
-                            __fmul_rn(code_value(p.fmt.code_type, e & 15), L));
-    }
+    for (int e = warp; e < 256; e += W)
+        *reinterpret_cast<float2*>(smem_raw + (tl - dyn) + 256 * e) =
+            make_float2(code_value(p.fmt.code_type, e >> 4), code_value(p.fmt.code_type, e & 15));
     for (int i = threadIdx.x; i < 256; i += S::THREADS)
         t8s[i] = dq_value(p.fmt.dq_type, (p.fmt.dq_type == 0 || i < 253) ? i : 0);
     const float off = p.dq ? *p.offset : 0.0f;
     __syncthreads();
 
     auto block_const = [&](float s, uint32_t q) {
-        return (p.dq ? __fadd_rn(__fmul_rn(t8s[q], s), off) : s) * p.inv_scale;
+        return p.dq ? __fadd_rn(__fmul_rn(t8s[q], s), off) : s;
     };
     // acc += the products of one block column
     auto block = [&](float (&acc)[4], const uint2& cg, const uint2& cu, const uint4 (&x)[2], float sg, float su) {
-        float d[4];
+        const uint64_t sg2 = twice(sg), su2 = twice(su);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const uint32_t wg = j < 2 ? cg.x : cg.y, wu = j < 2 ? cu.x : cu.y;
             const int k = 2 * (j & 1);
-            const uint32_t a0 = few_pair(wg, k, tl), a1 = few_pair(wu, k, tl);
-            const uint32_t a2 = few_pair(wg, k + 1, tl), a3 = few_pair(wu, k + 1, tl);
+            const uint32_t a0 = few_pair(wg, k, tl, sg2), a1 = few_pair(wu, k, tl, su2);
+            const uint32_t a2 = few_pair(wg, k + 1, tl, sg2), a3 = few_pair(wu, k + 1, tl, su2);
             const uint4 v = x[j >> 1];
-            if (j == 0)
-                mma_16816_z(d, a0, a1, a2, a3, v.x, v.y);
-            else
-                mma_16816(d, a0, a1, a2, a3, j & 1 ? v.z : v.x, j & 1 ? v.w : v.y);
+            mma_16816(acc, a0, a1, a2, a3, j & 1 ? v.z : v.x, j & 1 ? v.w : v.y);
         }
-        acc[0] = __fmaf_rn(sg, d[0], acc[0]);
-        acc[1] = __fmaf_rn(sg, d[1], acc[1]);
-        acc[2] = __fmaf_rn(su, d[2], acc[2]);
-        acc[3] = __fmaf_rn(su, d[3], acc[3]);
     };
 
     while (true) {

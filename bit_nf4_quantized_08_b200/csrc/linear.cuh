@@ -1020,11 +1020,11 @@ inline qlora_status linear_bwd_impl(const void* dY, const void* X, const LinearA
 // with cold caches: LLaMA-7B 128 / 129 tokens 113 / 111 us, LLaMA-65B 186 /
 // 285 us.
 constexpr int kGatedSmall = 128;
-// Most tokens of k_gated_few (its MMA's token side; with two token tiles a warp
-// LLaMA-65B took 147 us at 16 tokens against 133 us for k_gated_small,
-// LLaMA-7B 51 us against 50 us).  At 8 tokens it takes 84 us on LLaMA-65B
-// against 131 us, at one on LLaMA-7B 31 us against 49 us (whole calls, cold
-// caches).
+// Most tokens of k_gated_few (its MMA's token side).  Around it, whole calls
+// with cold caches, k_gated_few / k_gated_small: LLaMA-7B 39 / 49 us at one
+// token and 39 / 51 us at 8, LLaMA-65B 102 / 127 us and 106 / 129 us.  (With
+// two token tiles a warp and the cheaper rounded code book it was no faster
+// than k_gated_small at 16 tokens.)
 constexpr int kGatedFew = 8;
 
 struct BlockWs {
@@ -1115,7 +1115,6 @@ inline qlora_status gated_fwd_few(const void* X, const LinearArgs& a, const void
     p.kbs = (int)(a.K / 64);
     p.r = a.r;
     p.act = act;
-    p.inv_scale = 1.0f / (w.code_type ? 1.5f : 1.18881f);
     p.H = static_cast<uint16_t*>(H);
     p.GU = static_cast<uint16_t*>(GU);
     const int grid = (int)std::min<int64_t>(std::min(sm_count(), kSms), a.seg_rows / 8);

@@ -350,9 +350,8 @@ qlora_status qlora_fused_linear_dropout_bwd(const void *dY, const void *X, int64
  * K % 64 == 0, r % 8 == 0, 2r <= 256.  r == 0: no adapters.  M >= 0 (M == 0
  * writes dA = dB = 0 only).  An unknown act is INVALID_ARG.  Outputs and
  * inputs must not overlap.  (Where the workspace query gives 0, ws may be NULL.)
- * For M <= 8 the forward's weight operand is the rounded code book, the block
- * constants applied to each 64-element block's fp32 sum, as in the linear for
- * few tokens; for more it is the bf16 weight of qlora_nf4_dequantize.
+ * The weight operand is the bf16 weight of qlora_nf4_dequantize for every M, in
+ * the forward and the backward.
  */
 #define QLORA_ACT_SILU 0
 #define QLORA_ACT_GELU_TANH 1

@@ -61,3 +61,59 @@ def test_nan_token_gives_a_nan_row_and_no_other(Q, cuda, act, M):
     b = Q.qlora_gated_linear_fwd(X, q, t["A"], t["B"], 2.0, act, want_gu=True)
     for u, v in zip(a, b):
         assert _same_bits(u[rows], v[rows]) and bool(torch.isnan(v[M // 2]).all())
+
+
+def _gu64(Q, q, t, s, rows):
+    """The pre-activations of the first `rows` tokens from the definition in fp64, U rounded to bf16 as the layer's is."""
+    F, r = q.rows // 2, t["B"].shape[1]
+    X, A, B = (t[k].double() for k in ("X", "A", "B"))
+    U = (s * X[:rows] @ A.T).bfloat16().double()
+    Y = X[:rows] @ Q.qlora_nf4_dequantize(q).double().T
+    Y[:, :F] += U[:, :r] @ B[:F].T
+    Y[:, F:] += U[:, r:] @ B[F:].T
+    return Y
+
+
+@pytest.mark.parametrize("fmt", [dict(), dict(dq=False), dict(blocksize=128, code_type="fp4", dq_type="e4m3")],
+                         ids=["nf4", "no_dq", "fp4_128_e4m3"])
+@pytest.mark.parametrize("F,K", [(512, 704), (1024, 4096)])
+def test_few_tokens_compute_the_same_function_as_many(Q, cuda, F, K, fmt):
+    """A call of 8 tokens and the first 8 rows of calls of 9, 100 and 300: the same layer, so the same values up to the
+    order of fp32 sums.  Two fp32 sums of K <= 4096 bf16 products in different orders (tensor-core steps of 16 or 64)
+    differ by at most (K / 16) 2^-23 = 3e-5 of the sum of magnitudes' root mean square, 1e-4 of H behind the activation
+    and the product.  A value then lands on the other side of a rounding border with probability 1e-4 / 2^-7 = 1.3 %,
+    where it changes by 2^-7: sqrt(0.013) * 2^-7 = 9e-4 of the norm at most.  (sU is formed by another kernel past 16
+    tokens: one more such rounding on the adapter's term, below the base's size; 2e-3 there.)  No value moves by more
+    than one bf16 step of the largest of its terms: 2^-7 of the largest |value|."""
+    q, inp, _ = _setup(Q, 300, F, K, 16, seed=52, **fmt)
+    t = _dev(inp)
+    few = Q.qlora_gated_linear_fwd(t["X"][:8], q, t["A"], t["B"], 2.0, want_gu=True)
+    for M, tol in ((9, 1e-3), (100, 2e-3), (300, 2e-3)):
+        many = Q.qlora_gated_linear_fwd(t["X"][:M], q, t["A"], t["B"], 2.0, want_gu=True)
+        for name, a, b in zip(("H", "GU"), few, many):
+            a, b = a.double(), b[:8].double()
+            assert float((a - b).norm() / b.norm()) <= tol, (name, M)
+            assert float((a - b).abs().max()) <= 2.0 ** -7 * float(b.abs().max()), (name, M)
+    # against the definition: the output's own rounding, 2^-7 / sqrt(12) = 2.26e-3 of the norm if every value sat at
+    # the bottom of its binade (where a rounding weighs most), and the sums' 1e-4
+    ref = _gu64(Q, q, t, 2.0, 8)
+    assert float((few[1].double() - ref).norm() / ref.norm()) <= 2.4e-3
+    H = ref[:, :F] * torch.sigmoid(ref[:, :F]) * ref[:, F:]
+    assert float((few[0].double() - H).norm() / H.norm()) <= 2.4e-3
+    torch.cuda.synchronize()
+    assert Q.qlora_get_last_error() == 0
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("M", [1, 2, 7, 8])
+def test_few_tokens_weight_operand_is_the_dequantized_weight(Q, cuda, M, act):
+    """Tokens that are unit vectors read the weight back: without an adapter GU is W' itself, bit for bit."""
+    F, K = 512, 704
+    q, _, _ = _setup(Q, M, F, K, 0, seed=53)
+    W = Q.qlora_nf4_dequantize(q)
+    for k0 in (0, 17, 255, 256, 640, K - 8):
+        X = torch.zeros(M, K, dtype=torch.bfloat16, device=cuda)
+        cols = [(k0 + i) % K for i in range(M)]
+        X[torch.arange(M), cols] = 1.0
+        _, GU = Q.qlora_gated_linear_fwd(X, q, None, None, 1.0, act, want_gu=True)
+        assert torch.equal(GU, W[:, cols].T.contiguous()), k0
