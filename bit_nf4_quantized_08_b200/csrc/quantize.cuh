@@ -977,8 +977,11 @@ inline cudaError_t launch_expand_scales(const qlora_nf4_weight& w, float* scales
     const int64_t tiles = std::max<int64_t>(((w.rows + 31) / 32) * ((kbs + 31) / 32), nflags > 0 ? 1 : 0);
     if (tiles == 0) return cudaSuccess;
     note_launch();
-    // dependent launch: the CTAs can be resident before the kernel ahead
-    // ends and wait for it (pdl_wait) before any access
+    // dependent launch: the CTAs can be resident before the kernel ahead ends.
+    // They wait for it (pdl_wait) before any access, or, with beside, read the
+    // constants and write scales and flags at once and wait at their end; every
+    // CTA of the kernel ahead must then have waited for its own predecessors
+    // before it let this one start, and must touch neither scales nor flags
     return launch_pdl(k_expand_scales, dim3((unsigned)tiles), dim3(256), 0, s, 0, w.rows, kbs,
                       (int)w.double_quant, (const float*)w.absmax, (const uint8_t*)w.absmax_q8,
                       (const float*)w.absmax_scale, (const float*)w.absmax_offset, scales, ld, flags, nflags,

@@ -86,8 +86,9 @@ struct SkinnyParams {
 // Adapter dropout: the A tiles of X pass through mask warps between their TMA
 // load and the MMA.  A tile is 128 lines of 64 consecutive elements of X
 // (K-major: a token row each; MN-major: 64 tokens of each of two 64-column
-// chunks), eight generator blocks a line.  Three or four groups of four warps
-// take the k-steps in turn (the ring is a whole number of turns, so that a
+// chunks), eight generator blocks a line.  Groups of four warps, four of them
+// where the ring's stages are a multiple of four and else one a stage (three
+// or six), take the k-steps in turn (the ring is a whole number of turns, so that a
 // group always meets the same stages and its phase parities follow on), thread
 // t of a group line t: its eight masks are generated
 // before the tile is waited for, then each is ANDed onto one 16-byte chunk of

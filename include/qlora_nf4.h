@@ -311,7 +311,9 @@ qlora_status qlora_dropout(const void *X, qlora_dtype dtype, int64_t n, const ql
  *   Xd = keep * X,   U = s' Xd A^T,   Y[:, seg i] = X w'_i^T + U_i B_i^T
  *   G_i = s' dY[:, seg i] B_i,   dX = sum_i dY[:, seg i] w'_i + keep * (G A)
  *   dA = G^T Xd,   dB_i = dY[:, seg i]^T U_i
- * One mask serves every adapter of the projection.  Dropped elements of X
+ * One mask serves every adapter of the projection, where LoraConfig's
+ * lora_dropout draws one for each: for independent masks keep the linears as
+ * separate weights (nseg == 1), with an offset each.  Dropped elements of X
  * count as 0 in the adapter whatever they hold.  drop == NULL, or a
  * probability that rounds to 0, is no dropout.
  * grad_dtype: element type of dA and dB, fp32 (for qlora_adamw_step) or bf16
