@@ -4,7 +4,7 @@ and batches of more token tiles than SMs."""
 import pytest
 import torch
 
-from test_gpu_gated import _dev, _same_bits, _setup
+from test_gpu_gated import _check, _dev, _same_bits, _setup
 
 pytestmark = pytest.mark.gpu
 
@@ -117,3 +117,21 @@ def test_few_tokens_weight_operand_is_the_dequantized_weight(Q, cuda, M, act):
         X[torch.arange(M), cols] = 1.0
         _, GU = Q.qlora_gated_linear_fwd(X, q, None, None, 1.0, act, want_gu=True)
         assert torch.equal(GU, W[:, cols].T.contiguous()), k0
+
+
+@pytest.mark.parametrize("M,F,K,r", [
+    (8, 768, 448, 24), (9, 768, 448, 24),    # the last size of one kernel and the first of the next, tiles cut
+    (128, 768, 448, 24), (128, 1024, 256, 128),  # a full token tile
+    (129, 768, 448, 24),
+])
+@pytest.mark.parametrize("act,p", [("silu", 0.3), ("gelu_tanh", 0.0)])
+def test_borders_of_the_token_classes(Q, O, cuda, M, F, K, r, act, p):
+    q, inp, Wd = _setup(Q, M, F, K, r, seed=300 + M)
+    _check(Q, O, q, inp, Wd, 2.0, act, Q.Dropout(p, 31, 2) if p else None, f"border M={M} F={F} K={K} r={r} {act}")
+
+
+@pytest.mark.parametrize("M,p", [(9601, 0.2), (19001, 0.0)])
+def test_more_token_tiles_than_half_the_sms(Q, O, cuda, M, p):
+    """76 and 149 tiles of 128 tokens: the backward's first pass has one column range a tile and writes sG itself."""
+    q, inp, Wd = _setup(Q, M, 256, 64, 8, seed=54)
+    _check(Q, O, q, inp, Wd, 2.0, "silu", Q.Dropout(p, 8, 3) if p else None, f"M={M}")
