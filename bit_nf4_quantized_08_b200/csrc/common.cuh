@@ -323,6 +323,12 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&v)
         : "r"(taddr));
 }
 
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&v)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(taddr));
+}
+
 // The matching store: thread i of the warp writes lane (base lane + i).
 __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&v)[32]) {
     asm volatile(
@@ -396,6 +402,17 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     uint32_t d;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
     return d;
+}
+
+// Two fp32 values as the sum of two bf16 pairs: the values rounded, and what
+// the rounding left, rounded (2^-17 of the value).  Where a value rounds to an
+// infinity the remainder is 0, a NaN stays in the first pair.
+__device__ __forceinline__ void bf16_halves(float a, float b, uint32_t* hi, uint32_t* lo) {
+    const uint32_t h = pack_bf16x2(a, b);
+    const float ra = a - __uint_as_float(h << 16), rb = b - __uint_as_float(h & 0xFFFF0000u);
+    const float inf = __uint_as_float(0x7F800000u);
+    *hi = h;
+    *lo = pack_bf16x2(fabsf(ra) < inf ? ra : 0.0f, fabsf(rb) < inf ? rb : 0.0f);
 }
 
 __device__ __forceinline__ int elect_lane0() { return (threadIdx.x & 31) == 0; }

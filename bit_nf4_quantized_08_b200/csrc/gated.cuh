@@ -8,10 +8,11 @@
 // tanh form of GELU, g/2 (1 + t) with t = tanh(c (g + 0.044715 g^3)),
 // c = sqrt(2 / pi), act' = (1 + t) / 2 + g/2 (1 - t^2) c (1 + 3 * 0.044715 g^2).
 // All of it is formed in fp32.  Rounded to bf16 are H and the kept [g | u] (the
-// outputs), [dG | dU], U and G (the operands of the tensor-core products that
-// follow).  Each rounding adds 1.7e-3 of the norm to what it reaches, at most
-// three to a gradient: dA and dB are 2.9e-3 off their definition, dX 2.4e-3.
-// Two bf16 halves of an operand would halve that at twice its products.
+// outputs), and operands of the tensor-core products that follow: [dG | dU] for
+// dX and dB, G for dX and dA, U in the forward.  Each rounding adds 1.7e-3 of
+// the norm to what it reaches.  So that no gradient carries more than one
+// besides its own, as in the linear's backward, G is formed from dG and dU in
+// two bf16 halves each and dB from U in two.
 #pragma once
 
 #include <stdint.h>
@@ -67,10 +68,10 @@ __device__ __forceinline__ void act_value_grad(int act, float g, float* v, float
     *dv = s + x * (2.0f * 0.7978845608028654f) * (1.0f + 0.134145f * g2) * s * (1.0f - s);
 }
 
-// Eight columns of [dG | dU] from dH, g and u.
-template <int act>
-__device__ __forceinline__ void gated_grad8(const uint4& hv, const uint4& gv, const uint4& uv, uint32_t (&og)[4],
-                                            uint32_t (&ou)[4]) {
+// Eight columns of dG and dU from dH, g and u, one after the other: dG and dU
+// of columns 2 q and 2 q + 1 go to out(q, dG, dG', dU, dU').
+template <int act, class Out>
+__device__ __forceinline__ void gated_grad8(const uint4& hv, const uint4& gv, const uint4& uv, Out out) {
     const uint32_t h[4] = {hv.x, hv.y, hv.z, hv.w}, g[4] = {gv.x, gv.y, gv.z, gv.w}, u[4] = {uv.x, uv.y, uv.z, uv.w};
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -78,8 +79,7 @@ __device__ __forceinline__ void gated_grad8(const uint4& hv, const uint4& gv, co
         act_value_grad(act, bf16_lo(g[q]), &v0, &d0);
         act_value_grad(act, bf16_hi(g[q]), &v1, &d1);
         const float h0 = bf16_lo(h[q]), h1 = bf16_hi(h[q]);
-        og[q] = pack_bf16x2(h0 * bf16_lo(u[q]) * d0, h1 * bf16_hi(u[q]) * d1);
-        ou[q] = pack_bf16x2(h0 * v0, h1 * v1);
+        out(q, h0 * bf16_lo(u[q]) * d0, h1 * bf16_hi(u[q]) * d1, h0 * v0, h1 * v1);
     }
 }
 
@@ -96,10 +96,14 @@ __global__ void __launch_bounds__(256) k_gated_grad(const uint16_t* dH, const ui
         const uint4 gv = *reinterpret_cast<const uint4*>(GU + m * 2 * F + c * 8);
         const uint4 uv = *reinterpret_cast<const uint4*>(GU + m * 2 * F + F + c * 8);
         uint32_t og[4], ou[4];
+        auto out = [&](int q, float g0, float g1, float u0, float u1) {
+            og[q] = pack_bf16x2(g0, g1);
+            ou[q] = pack_bf16x2(u0, u1);
+        };
         if (act == ACT_SILU)
-            gated_grad8<ACT_SILU>(hv, gv, uv, og, ou);
+            gated_grad8<ACT_SILU>(hv, gv, uv, out);
         else
-            gated_grad8<ACT_GELU_TANH>(hv, gv, uv, og, ou);
+            gated_grad8<ACT_GELU_TANH>(hv, gv, uv, out);
         *reinterpret_cast<uint4*>(dGU + m * 2 * F + c * 8) = make_uint4(og[0], og[1], og[2], og[3]);
         *reinterpret_cast<uint4*>(dGU + m * 2 * F + F + c * 8) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
     }
@@ -109,21 +113,24 @@ __global__ void __launch_bounds__(256) k_gated_grad(const uint16_t* dH, const ui
 // The gated backward's first pass with adapters: dGU = [dH u act'(g) | dH act(g)]
 // as above, and sG = bf16(scale [dG B_gate | dU B_up]) from the tiles while
 // they are in shared memory, so that the second product does not read dGU back
-// (180 MB on LLaMA-65B at 2048 tokens).
+// (180 MB on LLaMA-65B at 2048 tokens) and can take the values to 16 bits: a
+// tile is followed by the remainders of its rounding, multiplied onto the same
+// sums.
 //
 // A CTA owns 128 tokens x a range of 64-column steps.  Per step sixteen warps
 // form dG and dU [128 x 64] from dH, g and u, which they load into registers
 // two steps ahead (96 KB in flight an SM: 2.2 us a step; with all three through
 // a TMA ring in shared memory, three steps deep, it was 3.2 us), and write them
-// to an operand stage; one thread stores the two tiles with TMA, one loads the
-// two adapters' B rows and one issues the tcgen05
-// products onto two accumulators [128 x r].  The column range is split over S
+// with their remainders to one of two operand stages; one thread stores the two
+// rounded tiles with TMA, one loads the two adapters' B rows and one issues the
+// tcgen05 products onto two accumulators [128 x r].  The column range is split over S
 // CTAs (about one CTA an SM in all), whose fp32 partial sums k_gated_sG adds in
 // split order (deterministic) and rounds once (added by each token tile's last
 // CTA instead, 590 KB through one SM, it took 26 us longer).
 // Bound by HBM: dH and g, u read, dGU written, 10 B per token and hidden
-// column (LLaMA-65B, 2048 tokens: 451 MB, 90 us, 5.0 TB/s; LLaMA-7B, 1997
-// tokens: 46 us).
+// column (LLaMA-65B, 2048 tokens: 451 MB, 101 us under the profiler, 4.5 TB/s;
+// LLaMA-7B, 1997 tokens: 54 us; 94 and 50 us without the remainders, in four
+// stages).
 // ---------------------------------------------------------------------------
 struct GatedGradParams {
     CUtensorMap tmDGU;  // dGU [M][2F], box {64, 128}
@@ -143,8 +150,9 @@ template <int BN>
 struct GatedGradShape {
     static constexpr int TILE = 128 * 128;   // 128 rows x 64 bf16
     static constexpr int B_BYTES = BN * 128;  // 64 rows x BN columns
-    static constexpr int STAGE = 2 * TILE + 2 * B_BYTES;
-    static constexpr int STAGES = BN <= 64 ? 4 : 3;
+    static constexpr int B_OFF = 4 * TILE;    // behind dG, dU and their remainders
+    static constexpr int STAGE = B_OFF + 2 * B_BYTES;
+    static constexpr int STAGES = 2;
     static constexpr int SMEM = STAGE * STAGES + 1024 + 256;
     static constexpr int CWARPS = 16;                    // compute warps
     static constexpr int THREADS = 32 * (3 + CWARPS);    // producer, MMA, store, compute
@@ -207,8 +215,8 @@ __global__ void __launch_bounds__(GatedGradShape<BN>::THREADS, 1)
                 const uint32_t st = base + s * S::STAGE;
                 mbar_arrive_expect_tx(full(s), 2 * S::B_BYTES);
                 for (int c = 0; c < BN / 64; ++c) {
-                    tma_load_2d(st + 2 * S::TILE + 8192 * c, &p.tmB, full(s), 64 * c, f);
-                    tma_load_2d(st + 2 * S::TILE + S::B_BYTES + 8192 * c, &p.tmB, full(s), 64 * c, p.F + f);
+                    tma_load_2d(st + S::B_OFF + 8192 * c, &p.tmB, full(s), 64 * c, f);
+                    tma_load_2d(st + S::B_OFF + S::B_BYTES + 8192 * c, &p.tmB, full(s), 64 * c, p.F + f);
                 }
                 last_use[s] = u;
             }
@@ -225,13 +233,14 @@ __global__ void __launch_bounds__(GatedGradShape<BN>::THREADS, 1)
                 if (!mbar_wait(full(s), u & 1, wc) || !mbar_wait(ready(s), u & 1, wc)) { *abort_flag = 1; break; }
                 tc_fence_after();
                 const uint32_t st = base + s * S::STAGE;
+                // tile t: dG, dU, then their remainders onto the same sums
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int t = 0; t < 4; ++t)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        umma_bf16(tmem + h * BN, smem_desc_sw128(st + h * S::TILE + kk * 32, 16, 1024),
-                                  smem_desc_sw128(st + 2 * S::TILE + h * S::B_BYTES + kk * 2048, 8192, 1024), idesc,
-                                  (i > 0 || kk > 0) ? 1u : 0u);
+                        umma_bf16(tmem + (t & 1) * BN, smem_desc_sw128(st + t * S::TILE + kk * 32, 16, 1024),
+                                  smem_desc_sw128(st + S::B_OFF + (t & 1) * S::B_BYTES + kk * 2048, 8192, 1024), idesc,
+                                  (i > 0 || kk > 0 || t > 1) ? 1u : 0u);
                 umma_commit(empty(s));
             }
             umma_commit(acc_full);
@@ -248,12 +257,9 @@ __global__ void __launch_bounds__(GatedGradShape<BN>::THREADS, 1)
                 tma_store_2d(&p.tmDGU, st, f, m0);
                 tma_store_2d(&p.tmDGU, st + S::TILE, p.F + f, m0);
                 bulk_commit_group();
-                // the step before has been read out of its stage
-                asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                if (i > 0) mbar_arrive(empty((i - 1) % STAGES));
+                bulk_wait_group_read0();  // the step has been read out of its stage
+                mbar_arrive(empty(s));
             }
-            bulk_wait_group_read0();
-            if (nk > 0 && !*abort_flag) mbar_arrive(empty((nk - 1) % STAGES));
             asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         }
     } else {
@@ -283,9 +289,6 @@ __global__ void __launch_bounds__(GatedGradShape<BN>::THREADS, 1)
             constexpr int act = decltype(act_tag)::value;
             auto step = [&](int i, const In& x) {
                 const int s = i % STAGES, u = i / STAGES;
-                uint32_t og[2][4], ou[2][4];
-                gated_grad8<act>(x.v[0], x.v[1], x.v[2], og[0], ou[0]);
-                gated_grad8<act>(x.v[3], x.v[4], x.v[5], og[1], ou[1]);
                 if (!__all_sync(0xffffffffu, mbar_wait(empty(s), (u & 1) ^ 1, wc))) {
                     *abort_flag = 1;
                     return false;
@@ -293,9 +296,15 @@ __global__ void __launch_bounds__(GatedGradShape<BN>::THREADS, 1)
                 const uint32_t st = base + s * S::STAGE;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
+                    uint32_t o[4][4];  // [dG, dU and their remainders][column pair]
+                    gated_grad8<act>(x.v[3 * h], x.v[3 * h + 1], x.v[3 * h + 2],
+                                     [&](int q, float g0, float g1, float u0, float u1) {
+                                         bf16_halves(g0, g1, &o[0][q], &o[2][q]);
+                                         bf16_halves(u0, u1, &o[1][q], &o[3][q]);
+                                     });
                     const uint32_t a = st + (uint32_t)(l + 64 * h) * 128u + (uint32_t)((c ^ (l & 7)) << 4);
-                    st_shared_v4(a, og[h][0], og[h][1], og[h][2], og[h][3]);
-                    st_shared_v4(a + S::TILE, ou[h][0], ou[h][1], ou[h][2], ou[h][3]);
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) st_shared_v4(a + t * S::TILE, o[t][0], o[t][1], o[t][2], o[t][3]);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();

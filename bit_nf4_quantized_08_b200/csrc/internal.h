@@ -81,6 +81,7 @@ struct LinearArgs {
     // (sG_part) or, unsplit, in the workspace
     int have_sG;
     const float* sG_part;
+    void* sU_halves;  // gated backward: sU in two bf16 halves [M][2 rt], in place of the workspace's sU
     int rt() const { return r * nseg; }  // columns of sU and sG
 };
 qlora_status linear_fwd_impl(const void* X, const LinearArgs& a, const void* A, const void* B,

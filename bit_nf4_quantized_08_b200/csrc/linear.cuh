@@ -191,6 +191,7 @@ struct SkinnyDesc {
     int64_t out_ld;
     int r;         // output columns (0: the launch's r)
     int seg_mode, seg_rows, seg_r;  // SK_SEG_* (fused projections)
+    int halves;    // SK_HALVES_*
     const DropParams* drop;  // the A operand is X under this dropout, or null
     int64_t drop_cols;       // X's row length
 };
@@ -248,6 +249,7 @@ inline qlora_status skinny(const SkinnyDesc* d, int nprob, int r, cudaStream_t s
         q.seg_mode = d[i].seg_mode;
         q.seg_rows = d[i].seg_rows;
         q.seg_r = d[i].seg_r;
+        q.halves = d[i].halves;
         q.ksteps = d[i].ksteps;
         q.tiles = ceil_div(d[i].rows, 128);
         q.scale = d[i].scale;
@@ -754,6 +756,18 @@ inline bool desc_sG(SkinnyDesc* d, const CUtensorMap& tdY, const LinearArgs& a, 
     return true;
 }
 
+// sU for dB: the workspace's bf16 sU, or in two halves (each adapter's columns
+// and then their remainders).
+inline bool desc_sU_bwd(SkinnyDesc* d, const void* X, const LinearArgs& a, const void* A, const LinearWs& L) {
+    if (!desc_sU(d, X, a, A, a.sU_halves ? a.sU_halves : L.sU)) return false;
+    if (a.sU_halves) {
+        d->halves = SK_HALVES_OUT;
+        d->seg_r = a.r;
+        d->out_ld = 2 * a.rt();
+    }
+    return true;
+}
+
 // dA^T [K][r] = X^T sG : Aop = X viewed [k][m] (MN-major), Bop = sG viewed [j][m] (MN-major)
 // dB [N][r] = dY^T sU : Aop = dY viewed [n][m] (MN-major), Bop = sU viewed [j][m]
 inline bool desc_dA_dB(SkinnyDesc* d, const void* dY, const void* X, const LinearArgs& a, const LinearWs& L,
@@ -769,7 +783,9 @@ inline bool desc_dA_dB(SkinnyDesc* d, const void* dY, const void* X, const Linea
     d[0].out_ld = a.K;
     d[0].r = a.rt();
     if (!map_bf16(&d[1].tA, dY, a.N, a.M, 64)) return false;
-    if (!map_bf16(&d[1].tB, L.sU, a.rt(), a.M, 64)) return false;
+    const int h = a.sU_halves ? 2 : 1;
+    if (!map_bf16(&d[1].tB, a.sU_halves ? a.sU_halves : L.sU, h * a.rt(), a.M, 64)) return false;
+    d[1].halves = a.sU_halves ? SK_HALVES_IN : SK_HALVES_NONE;
     d[1].rows = (int)a.N;
     d[1].out_mode = a.grad_bf16 ? SK_OUT_BF16 : SK_OUT_F32;
     d[1].out = dB;
@@ -778,7 +794,7 @@ inline bool desc_dA_dB(SkinnyDesc* d, const void* dY, const void* X, const Linea
     if (a.nseg > 1) {  // the dB rows of a segment read that segment's sU columns
         d[1].seg_mode = SK_SEG_ROWS;
         d[1].seg_rows = (int)a.seg_rows;
-        d[1].seg_r = a.r;
+        d[1].seg_r = h * a.r;
     }
     for (int i = 0; i < 2; ++i) {
         d[i].a_mn = 1;
@@ -899,7 +915,7 @@ inline qlora_status linear_bwd_forked(const void* dY, const void* X, const Linea
     if (!a.have_sG) {
         SkinnyDesc d2[2];
         if (!desc_sG(&d2[sU_first ? 1 : 0], tdY, a, B, L.sG)) return QLORA_ERR_CUDA;
-        if (sU_first && !desc_sU(&d2[0], X, a, A, L.sU)) return QLORA_ERR_CUDA;
+        if (sU_first && !desc_sU_bwd(&d2[0], X, a, A, L)) return QLORA_ERR_CUDA;
         st = skinny(d2, sU_first ? 2 : 1, a.rt(), s, 1, a.drop ? SKP_SPLIT : SKP_PACKED);
         if (st != QLORA_OK) return st;
         // under dropout the dX GEMM waits for this launch in any case: the
@@ -918,7 +934,7 @@ inline qlora_status linear_bwd_forked(const void* dY, const void* X, const Linea
     // runs, the rest start as it ends.  sU tiles (inputs only) start at once,
     // dA tiles wait for sG (the kernel before), dB tiles for the sU tiles.
     SkinnyDesc d3[3];
-    if (st == QLORA_OK && !desc_sU(&d3[0], X, a, A, L.sU)) st = QLORA_ERR_CUDA;
+    if (st == QLORA_OK && !desc_sU_bwd(&d3[0], X, a, A, L)) st = QLORA_ERR_CUDA;
     if (st == QLORA_OK && !desc_dA_dB(d3 + 1, dY, X, a, L, dA, dB)) st = QLORA_ERR_CUDA;
     // (have_sG: dY, sG and the zeroed counters come from the kernel before;
     // dropout: sG, the counters and perhaps sU do)
@@ -991,7 +1007,7 @@ inline qlora_status linear_bwd_impl(const void* dY, const void* X, const LinearA
     // serial path: sU and sG in one launch, dX GEMM, dA and dB
     if (a.r > 0) {
         SkinnyDesc d[2];
-        if (!desc_sU(&d[0], X, a, A, L.sU)) return QLORA_ERR_CUDA;
+        if (!desc_sU_bwd(&d[0], X, a, A, L)) return QLORA_ERR_CUDA;
         if (!a.have_sG && !desc_sG(&d[1], tdY, a, B, L.sG)) return QLORA_ERR_CUDA;
         // waits for the kernel before (the expansion, a dependent launch that
         // lets this one start early) before it loads: the workspace it writes
@@ -1016,8 +1032,8 @@ inline qlora_status linear_bwd_impl(const void* dY, const void* X, const LinearA
 // ---------------------------------------------------------------------------
 // The gated feed-forward.  Workspace: forward, sU and, for 9 to 128 tokens, the
 // partial tiles and their arrival counters, for more the expanded block constants;
-// backward, the linear's, the gradient of the pre-activations [M, 2F] and the
-// split partial sums of sG.
+// backward, the linear's, the gradient of the pre-activations [M, 2F], sU in two
+// bf16 halves and the split partial sums of sG.
 // ---------------------------------------------------------------------------
 // Most tokens of k_gated_small (its MMA's token side).  Around it, whole calls
 // with cold caches: LLaMA-7B 128 / 129 tokens 113 / 111 us, LLaMA-65B 186 /
@@ -1035,6 +1051,7 @@ struct BlockWs {
     size_t linear_bytes;
     uint16_t* gu;
     float* grad_part;
+    uint16_t* sU_halves;
     uint16_t* sU;
     float* scales;  // [K/64][N]
     float* part;
@@ -1066,6 +1083,7 @@ inline BlockWs carve_block_ws(void* ws, int64_t M, int64_t N, int64_t K, int rt,
     b.linear_bytes = linear_workspace_bytes(M, N, K, rt, bwd);
     b.linear = c.take(b.linear_bytes);
     b.gu = static_cast<uint16_t*>(c.take((size_t)M * N * 2));
+    if (rt > 0) b.sU_halves = static_cast<uint16_t*>(c.take((size_t)M * 2 * rt * 2));
     const int S = gated_splits(M, N / 2);
     if (rt > 0 && S > 1) b.grad_part = static_cast<float*>(c.take((size_t)((M + 127) / 128) * S * 128 * rt * 4));
     b.bytes = c.used;
@@ -1288,6 +1306,7 @@ inline qlora_status gated_bwd_impl(const void* dH, const void* X, const void* GU
         if (st != QLORA_OK) return st;
         a.have_sG = a.r > 0 ? 1 : 0;
         a.sG_part = b.grad_part;
+        a.sU_halves = b.sU_halves;
     }
     return linear_bwd_impl(b.gu, X, a, A, B, dX, dA, dB, b.linear, b.linear_bytes, s);
 }

@@ -46,7 +46,13 @@ struct SkinnyProblem {
     // the load's zero fill.
     int seg_mode, seg_rows, seg_r;
     int drop;  // the A operand is X under dropout: masked in shared memory (DROP kernels)
+    // An operand in two bf16 halves (common.cuh, bf16_halves).  SK_HALVES_OUT
+    // (a bf16 row-major output): every seg_r columns are followed by their
+    // remainders.  SK_HALVES_IN (a row-major output): the B operand has 2 r
+    // columns, and output column j is the sum of columns j and j + r.
+    int halves;
 };
+enum { SK_HALVES_NONE = 0, SK_HALVES_OUT = 1, SK_HALVES_IN = 2 };
 
 enum { SK_SEG_NONE = 0, SK_SEG_REDUCE = 1, SK_SEG_ROWS = 2 };
 
@@ -198,7 +204,8 @@ __global__ void __launch_bounds__(SkinnyShape<BN, DROP>::THREADS, 1) k_skinny(co
     const int k1 = spare ? k0 : min(P.ksteps, k0 + P.per);
     const int nk = k1 > k0 ? k1 - k0 : 0;
     const int rows_per = 128 / cs;  // tile rows owned by each rank
-    const int rc = (P.r + 3) & ~3;  // columns sent per row
+    const int cols = P.halves == SK_HALVES_IN ? 2 * P.r : P.r;
+    const int rc = (cols + 3) & ~3;  // columns sent per row
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -384,13 +391,16 @@ __global__ void __launch_bounds__(SkinnyShape<BN, DROP>::THREADS, 1) k_skinny(co
             for (int e = t; e < nrows * r4; e += 128) {
                 const int rr = e / r4, j = (e - rr * r4) * 4;
                 float4 acc = *reinterpret_cast<const float4*>(&red[rr * LD + j]);
-                for (int zz = 1; zz < cs; ++zz) {
-                    const float4 b = *reinterpret_cast<const float4*>(&red[(zz * rows_per + rr) * LD + j]);
+                auto add = [&](int at) {
+                    const float4 b = *reinterpret_cast<const float4*>(&red[at]);
                     acc.x = __fadd_rn(acc.x, b.x);
                     acc.y = __fadd_rn(acc.y, b.y);
                     acc.z = __fadd_rn(acc.z, b.z);
                     acc.w = __fadd_rn(acc.w, b.w);
-                }
+                };
+                for (int zz = 1; zz < cs; ++zz) add((zz * rows_per + rr) * LD + j);
+                if (P.halves == SK_HALVES_IN)
+                    for (int zz = 0; zz < cs; ++zz) add((zz * rows_per + rr) * LD + j + P.r);
                 acc.x = __fmul_rn(acc.x, P.scale);
                 acc.y = __fmul_rn(acc.y, P.scale);
                 acc.z = __fmul_rn(acc.z, P.scale);
@@ -398,6 +408,13 @@ __global__ void __launch_bounds__(SkinnyShape<BN, DROP>::THREADS, 1) k_skinny(co
                 const int64_t o = (int64_t)(m0 + r0 + rr) * P.out_ld + j;
                 if (P.out_mode == SK_OUT_F32) {
                     *reinterpret_cast<float4*>(static_cast<float*>(P.out) + o) = acc;
+                } else if (P.halves == SK_HALVES_OUT) {
+                    uint2 h, l;
+                    bf16_halves(acc.x, acc.y, &h.x, &l.x);
+                    bf16_halves(acc.z, acc.w, &h.y, &l.y);
+                    uint16_t* out = static_cast<uint16_t*>(P.out) + o + j / P.seg_r * P.seg_r;
+                    *reinterpret_cast<uint2*>(out) = h;
+                    *reinterpret_cast<uint2*>(out + P.seg_r) = l;
                 } else {
                     uint2 h;
                     h.x = pack_bf16x2(acc.x, acc.y);
@@ -704,6 +721,17 @@ __global__ void __launch_bounds__(StreamShape<BN, DROP>::THREADS, 1)
                 __syncwarp();
                 tmem_ld_32x32b_x32(taddr + (uint32_t)c0, v);
                 tmem_ld_wait();
+                if (P.halves == SK_HALVES_IN) {  // (r <= BN / 2: the columns exist)
+#pragma unroll
+                    for (int q = 0; q < 32; q += 8) {
+                        uint32_t w[8];
+                        tmem_ld_32x32b_x8(taddr + (uint32_t)(c0 + P.r + q), w);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            v[q + i] = __float_as_uint(__fadd_rn(__uint_as_float(v[q + i]), __uint_as_float(w[i])));
+                    }
+                }
                 if (!live) continue;
                 if (P.out_mode == SK_OUT_F32_T) {
                     float* out = static_cast<float*>(P.out);
@@ -728,6 +756,20 @@ __global__ void __launch_bounds__(StreamShape<BN, DROP>::THREADS, 1)
                                             __fmul_rn(__uint_as_float(v[q + 1]), P.scale),
                                             __fmul_rn(__uint_as_float(v[q + 2]), P.scale),
                                             __fmul_rn(__uint_as_float(v[q + 3]), P.scale));
+                } else if (P.halves == SK_HALVES_OUT) {
+                    uint16_t* out = static_cast<uint16_t*>(P.out) + (int64_t)m * P.out_ld;
+#pragma unroll
+                    for (int q = 0; q < 32; q += 8)  // (seg_r is a multiple of 8)
+                        if (c0 + q < P.r) {
+                            uint32_t h[4], l[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                bf16_halves(__fmul_rn(__uint_as_float(v[q + 2 * i]), P.scale),
+                                            __fmul_rn(__uint_as_float(v[q + 2 * i + 1]), P.scale), &h[i], &l[i]);
+                            uint16_t* o = out + c0 + q + (c0 + q) / P.seg_r * P.seg_r;
+                            *reinterpret_cast<uint4*>(o) = make_uint4(h[0], h[1], h[2], h[3]);
+                            *reinterpret_cast<uint4*>(o + P.seg_r) = make_uint4(l[0], l[1], l[2], l[3]);
+                        }
                 } else {
                     uint16_t* out = static_cast<uint16_t*>(P.out) + (int64_t)m * P.out_ld;
 #pragma unroll

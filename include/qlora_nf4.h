@@ -345,8 +345,9 @@ qlora_status qlora_fused_linear_dropout_bwd(const void *dY, const void *X, int64
  * act: QLORA_ACT_SILU, g / (1 + exp(-g)), or QLORA_ACT_GELU_TANH,
  * g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))).
  * Backward, from dH [M, F] and the kept GU:
- *   dY = [dH u act'(g) | dH act(g)] (rounded to bf16),
- *   dX, dA, dB = those of qlora_fused_linear_dropout_bwd for this dY.
+ *   dY = [dH u act'(g) | dH act(g)],
+ *   dX, dA, dB = those of qlora_fused_linear_dropout_bwd for this dY, which is
+ *   rounded to bf16 for dX and dB, not for G; dB takes U in two bf16 halves.
  *   dX may be NULL.  grad_dtype as above.
  * A [2r, K], B [2F, r].  Requirements of the fused projection: F % 256 == 0,
  * K % 64 == 0, r % 8 == 0, 2r <= 256.  r == 0: no adapters.  M >= 0 (M == 0

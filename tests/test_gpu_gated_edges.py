@@ -135,3 +135,58 @@ def test_more_token_tiles_than_half_the_sms(Q, O, cuda, M, p):
     """76 and 149 tiles of 128 tokens: the backward's first pass has one column range a tile and writes sG itself."""
     q, inp, Wd = _setup(Q, M, 256, 64, 8, seed=54)
     _check(Q, O, q, inp, Wd, 2.0, "silu", Q.Dropout(p, 8, 3) if p else None, f"M={M}")
+
+
+@pytest.mark.parametrize("M,F,K,r,p", [(8, 512, 320, 16, 0.0), (200, 768, 448, 24, 0.2), (700, 512, 576, 64, 0.0),
+                                       (700, 512, 320, 72, 0.1), (300, 512, 256, 128, 0.0), (9601, 256, 64, 32, 0.0)])
+@pytest.mark.parametrize("serial", [False, True])
+def test_adapter_gradients_carry_one_rounding(Q, cuda, M, F, K, r, p, serial):
+    """dA and dB in fp32 against the gradient at the kept [g | u] in fp64.  dA carries G's rounding to bf16 and dB that
+    of dY, one each: a bf16 rounding is uniform over a step of 2^-7 of the value's binade, 2^-7 / sqrt(12) of it, and a
+    value's mean square over its binade is 2.16 for the logarithmic distribution of significands: 1.53e-3 of the norm,
+    1.7e-3 where large values weigh most.  Two such roundings are 2.2e-3 to 2.4e-3, so the border is 1.95e-3; over
+    5000 and more independent roundings the fluctuation is below 2 %.  (M = 8: G has 256 values only, 2.1e-3.)"""
+    q, inp, _ = _setup(Q, M, F, K, r, seed=55)
+    t = _dev(inp)
+    drop = Q.Dropout(p, 3, 7) if p else None
+    _, GU = Q.qlora_gated_linear_fwd(t["X"], q, t["A"], t["B"], 2.0, "silu", drop, want_gu=True)
+    Q.qlora_debug_inject(6 if serial else 0)
+    try:
+        dX, dA, dB = Q.qlora_gated_linear_bwd(t["dH"], t["X"], GU, q, t["A"], t["B"], 2.0, "silu", drop)
+    finally:
+        Q.qlora_debug_inject(0)
+    torch.cuda.synchronize()
+    assert Q.qlora_get_last_error() == 0
+    X, A, B, dH, GU = (x.double() for x in (t["X"], t["A"], t["B"], t["dH"], GU))
+    mask = torch.ones_like(X) if drop is None else \
+        Q.qlora_dropout(torch.ones(M, K, device=cuda), drop).double().sign()
+    s = 2.0 * (1.0 if drop is None else 32768 / (32768 - int(p * 32768 + 0.5)))
+    g, u = GU[:, :F], GU[:, F:]
+    sig = torch.sigmoid(g)
+    dY = torch.cat([dH * u * sig * (1 + g * (1 - sig)), dH * g * sig], dim=1)
+    G = s * torch.cat([dY[:, :F] @ B[:F], dY[:, F:] @ B[F:]], dim=1)
+    U = s * (X * mask) @ A.T
+    rA = G.T @ (X * mask)
+    rB = torch.cat([dY[:, :F].T @ U[:, :r], dY[:, F:].T @ U[:, r:]])
+    bound = 1.95e-3 if M > 8 else 2.1e-3
+    assert float((dA - rA).norm() / rA.norm()) <= bound, "dA"
+    assert float((dB - rB).norm() / rB.norm()) <= bound, "dB"
+
+
+@pytest.mark.parametrize("M", [5, 300])
+def test_gradient_values_that_round_to_infinity(Q, cuda, M):
+    """dG of 2^127 times 1.999: bf16 rounds it to infinity, and its remainder must not turn the infinity into a NaN:
+    sG of that token is infinite, not NaN, so dA's gate columns are infinite where X is not 0."""
+    F, K, r = 256, 128, 8
+    q, inp, _ = _setup(Q, M, F, K, r, seed=56)
+    t = _dev(inp)
+    GU = torch.zeros(M, 2 * F, dtype=torch.bfloat16, device=cuda)
+    GU[:, :F] = 100.0  # silu'(100) = 1, so dG = dH u
+    dH = torch.zeros(M, F, dtype=torch.bfloat16, device=cuda)
+    GU[0, F + 3], dH[0, 3] = 2.0 ** 64 * 1.9921875, 2.0 ** 63 * 1.9921875  # product 2^127 * 3.97: over
+    B = torch.ones_like(t["B"])
+    X = torch.ones_like(t["X"])
+    dX, dA, dB = Q.qlora_gated_linear_bwd(dH, X, GU, q, t["A"], B, 1.0)
+    torch.cuda.synchronize()
+    assert Q.qlora_get_last_error() == 0
+    assert bool(torch.isinf(dA[:r]).all())
