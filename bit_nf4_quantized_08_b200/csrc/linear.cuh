@@ -590,8 +590,13 @@ inline qlora_status launch_small_m(const void* X, const LinearArgs& a, const voi
                                    const LinearWs& L, cudaStream_t s) {
     // M <= 16: the warp-MMA kernel (test mode 8: the tcgen05 kernel instead);
     // 17 <= M <= 32: the tcgen05 kernel (test mode 7: the warp-MMA kernel)
+    // Under adapter dropout, that is in training, the tcgen05 kernel for every
+    // M: it multiplies with the bf16 weight that the backward differentiates,
+    // not with the rounded code book.  (Whole calls at 16 tokens, cold caches,
+    // tcgen05 / warp-MMA: 256 x 256 12 / 16 us, 4096 x 4096 27 / 33 us, q/k/v
+    // of 8192 x 8192 104 / 84 us, 8192 x 22016 111 / 84 us.)
     const int mode = inject_mode();
-    if ((a.M <= kSmallMmaDefault && mode != 8) || (a.M <= kSmallMma && mode == 7))
+    if ((a.M <= kSmallMmaDefault && mode != 8 && !a.drop) || (a.M <= kSmallMma && mode == 7))
         return launch_small_m_mma(X, a, B, Y, L, s);
     const qlora_nf4_weight& w = *a.w;
     const int NT = small_m_nt(a.M);
@@ -644,9 +649,9 @@ inline qlora_status launch_small_m(const void* X, const LinearArgs& a, const voi
 
 // sU for up to 16 tokens (the MMA's token side).  Under dropout every CTA forms
 // the whole mask, where the cluster GEMM splits it; whole calls of the linear,
-// k_small_u / masked cluster GEMM, cold caches: 256 x 256 at 16 tokens 16 / 18
-// us, 4096 x 4096 33 / 43 us, 4096 x 11008 47 / 55 us, q/k/v of 8192 x 8192 84 /
-// 94 us, 8192 x 22016 84 / 92 us, and at one token there 74 / 92 us.
+// k_small_u / masked cluster GEMM, cold caches: 256 x 256 at 16 tokens 12 / 14
+// us, 4096 x 4096 27 / 33 us, 4096 x 11008 47 / 53 us, q/k/v of 8192 x 8192 104
+// / 117 us, 8192 x 22016 111 / 119 us, and at one token there 99 / 119 us.
 constexpr int kSmallU = 16;
 inline qlora_status launch_small_u(const void* X, const LinearArgs& a, const void* A, uint16_t* sU, cudaStream_t s) {
     ProfileScope ps(QLORA_KERNEL_LORA_GEMM, s);

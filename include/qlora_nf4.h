@@ -315,7 +315,10 @@ qlora_status qlora_dropout(const void *X, qlora_dtype dtype, int64_t n, const ql
  * lora_dropout draws one for each: for independent masks keep the linears as
  * separate weights (nseg == 1), with an offset each.  Dropped elements of X
  * count as 0 in the adapter whatever they hold.  drop == NULL, or a
- * probability that rounds to 0, is no dropout.
+ * probability that rounds to 0, is no dropout: the values of
+ * qlora_fused_linear_fwd / _bwd, which for few tokens multiplies with a rounded
+ * code book; with a dropout the weight operand is the bf16 weight of
+ * qlora_nf4_dequantize for every M.
  * grad_dtype: element type of dA and dB, fp32 (for qlora_adamw_step) or bf16
  * (the adapters' own type).  dX may be NULL.  With M == 0, dA and dB are set
  * to zero.  Other arguments, requirements, streams and errors as for
